@@ -83,6 +83,12 @@ def lib() -> ctypes.CDLL:
         L.int4_matmul_workspace_size.argtypes = [i32, i64, i32, i64, i64, ctypes.POINTER(sz)]
         L.int4_matmul_select.argtypes = [i32, i64, i32, i64, i64]
         L.int4_matmul_decode_noalloc.argtypes = [vp, i32, vp, vp, i64, i32, i64, i64, vp, vp]
+        L.int4_cache_write.argtypes = [vp, vp, i64, i64, vp, i64, i64, i32, i64, vp, vp]
+        L.int4_cache_read.argtypes = [vp, vp, i64, vp, vp, i32, vp]
+        L.int4_cache_attention.argtypes = [vp, vp, i64, i64, i32, i64, i32, vp, i64, i32, vp, vp, i32,
+                                           i32, i32, ctypes.c_float, vp, vp, i32, vp, sz, vp]
+        L.int4_cache_attention_workspace_size.argtypes = [vp, i32, i64, i32, i32, i32, i32,
+                                                          ctypes.POINTER(sz)]
         L.int4_device_status.argtypes = [vp]
         L.int4_selftest_wait_timeout.argtypes = [u32, vp]
         L.int4_last_error.restype = ctypes.c_char_p
@@ -93,6 +99,8 @@ def lib() -> ctypes.CDLL:
                      "int4_dequantize_affine",
                      "int4_matmul_ws", "int4_matmul_workspace_size", "int4_matmul_decode_noalloc",
                      "int4_matmul_select", "int4_device_status", "int4_selftest_wait_timeout",
+                     "int4_cache_write", "int4_cache_read", "int4_cache_attention",
+                     "int4_cache_attention_workspace_size",
                      "int4_version"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -404,5 +412,8 @@ def selftest_wait_timeout(spins: int, device=None) -> None:
 
 
 from .module import Int4Linear  # noqa: E402  (uses the functions above)
+from .cache import (Int4KVCache, cache_attention_workspace_size, int4_cache_attention,  # noqa: E402
+                    int4_cache_read, int4_cache_write)
 
-__all__.append("Int4Linear")
+__all__ += ["Int4Linear", "Int4KVCache", "int4_cache_write", "int4_cache_read",
+            "int4_cache_attention", "cache_attention_workspace_size"]

@@ -1,0 +1,990 @@
+// Attention over the 4-bit cache for few query rows (decoding, and chunks of
+// queries): the tensor-core kernel and the kernel that joins its pieces.
+//
+// Mathematics.  For the RT query rows that share one key/value head (the
+// query heads of the group times the sequence's query tokens), per tile of
+// tokens:
+//   S^T = K Q^T          mma.m16n8k16, tokens x query rows
+//   P   = 2^(S - max)    running maximum and sum per row, in fp32
+//   O^T += V^T P^T       mma.m16n8k16, head elements x query rows
+// The codes enter the products as they are: a nibble n (offset to 0..15) in
+// the low bits of a half is the fp16 subnormal n 2^-24, which the tensor core
+// multiplies exactly, so expanding 8 codes takes a shift and four bitwise
+// operations and no arithmetic.  The second nibble of a byte stays four bits
+// up and counts 16-fold; the query's element (or the output row) is divided
+// by 16 instead, exactly.  With z the zero point (8 in the symmetric scheme,
+// whose codes are turned to 0..15 by flipping the sign bit)
+//   sum_d q_d (n_d - z) s = s (sum_d q_d n_d - z sum_d q_d), per group, and
+//   sum_t p_t s_t (n_t - z_t) = sum_t w_t n_t - sum_t w_t z_t, w_t = p_t s_t,
+// the second sum by one more matrix product whose A operand holds the z_t.
+//
+// Precision.  q enters in fp16 after a power-of-two scaling by the row's
+// largest element: exact for bf16 and fp16 but for elements 2^-24 times
+// smaller than that one, whose error stays below 2^-38 of it.  S, the
+// softmax's maximum and sum and O are fp32.  w_t is rounded to fp16 (2^-11
+// relative), scaled by a power of two that follows the tile's largest value
+// scale, so that weights down to 2^-29 of the largest keep their full
+// precision; the output type rounds coarser than the sum of these errors.
+//
+// Layout.  One warp takes 32 tokens at a time: their key and value rows are
+// copied to shared memory by 16-byte asynchronous copies, several tiles
+// ahead, each warp on its own.  ldmatrix then gives each lane whole words of
+// a token's codes (keys), and its transposed form gives halfwords of two
+// neighbouring tokens (values), which are the A operands after the bitwise
+// expansion: the contraction order inside a block of 32 elements is permuted
+// and Q is stored in the same order.
+//
+// Work split.  The tokens of all (sequence, head, row tile) items are counted
+// in steps of 128 and shared evenly among one wave of blocks, whatever the
+// lengths; a block's share may begin or end inside an item, and the pieces of
+// a split item are joined by a second kernel in a fixed order.  Every block
+// finds its share from the lengths on the device, so a captured graph can be
+// replayed with other lengths.
+#pragma once
+
+#include "cache.cuh"
+#include "internal.h"
+#include "sm100_ptx.cuh"
+
+namespace int4lib {
+
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnTokens = 32;                        // tokens of a warp's tile
+constexpr int kAttnStep = kAttnWarps * kAttnTokens;    // tokens of a block's step
+
+// Where the pieces of split items go, in the caller's workspace.
+inline size_t attention_prefix_bytes(int64_t batch) {
+  return (static_cast<size_t>(batch + 1) * 8 + 255) / 256 * 256;
+}
+struct AttentionSpace {
+  int64_t* prefix;  // [batch + 1]: units of the sequences before each
+  float* o;         // [2 * blocks][RT][D]: sums relative to the piece's maximum
+  float* ml;        // [2 * blocks][RT][2]: maximum (log2) and sum
+  int blocks;
+};
+
+// Row tile `rt` (rows [rt RT, (rt + 1) RT) of a sequence's query tokens x
+// ratio): the tokens it needs, from lo (a multiple of 32) to hi, and its
+// steps.
+struct RowTile {
+  int lo, hi, steps;
+  __device__ __forceinline__ void set(const AttentionArgs& a, int64_t len, int64_t count, int rt, int RT) {
+    const int64_t r0 = static_cast<int64_t>(rt) * RT;
+    const int64_t rows = count * a.ratio;
+    const int64_t r1 = (r0 + RT < rows ? r0 + RT : rows) - 1;
+    int64_t lo0, hi0, lo1, hi1;
+    a.visible(len - count + r0 / a.ratio, len, lo0, hi0);
+    a.visible(len - count + r1 / a.ratio, len, lo1, hi1);
+    lo = static_cast<int>(lo0) & ~(kAttnTokens - 1);
+    hi = static_cast<int>(hi1);
+    steps = hi > lo ? (hi - lo + kAttnStep - 1) / kAttnStep : 0;
+  }
+};
+
+__device__ __forceinline__ int row_tiles(const AttentionArgs& a, int64_t count, int RT) {
+  return static_cast<int>((count * a.ratio + RT - 1) / RT);
+}
+
+// Steps of one head of sequence b, over all its row tiles.
+__device__ __forceinline__ int64_t head_units(const AttentionArgs& a, int b, int RT) {
+  int64_t first, count;
+  a.queries(b, first, count);
+  const int64_t len = a.kv_len(b);
+  const int n = row_tiles(a, count, RT);
+  int64_t u = 0;
+  for (int rt = 0; rt < n; ++rt) {
+    RowTile r;
+    r.set(a, len, count, rt, RT);
+    u += r.steps;
+  }
+  return u;
+}
+
+// Blocks that take part, and the first unit of block c, when there are
+// `units` in all.
+__device__ __forceinline__ int64_t active_blocks(int64_t units, int blocks) {
+  return units < blocks ? units : blocks;
+}
+__device__ __forceinline__ int64_t share_begin(int64_t units, int64_t active, int64_t c) {
+  return c * units / active;
+}
+// The block whose share holds unit u: the largest c with c units / active <= u.
+__device__ __forceinline__ int64_t share_of(int64_t units, int64_t active, int64_t u) {
+  return ((u + 1) * active - 1) / units;
+}
+
+template <int D_, int GROUP_, int NT_, bool ASYM_>
+struct AttnCfg {
+  static constexpr int D = D_, GROUP = GROUP_, NT = NT_;
+  static constexpr bool ASYM = ASYM_;
+  static constexpr int RT = 8 * NT;            // query rows of a tile
+  static constexpr int DB = D / 32;            // blocks of 32 elements
+  static constexpr int NG = D / GROUP;         // groups of a row
+  static constexpr int BPG = GROUP / 32;       // blocks of a group
+  static constexpr int RB = D / 2;             // bytes of a row
+  static constexpr int RC = RB / 16;           // 16-byte chunks of a row
+  // Blocks on an SM, by the registers of the accumulators (D / 4 NT a lane).
+  static constexpr int kBlocks = D * NT <= 128 ? 4 : (D * NT <= 256 ? 3 : 2);
+  // One warp's tile: keys, values, their scales, their zero points.
+  static constexpr int kCodes = kAttnTokens * RB;
+  static constexpr int kScales = kAttnTokens * NG * 2;
+  static constexpr int kZeros = ASYM ? kAttnTokens * NG : 0;
+  static constexpr int kScaleAt = 2 * kCodes;
+  static constexpr int kZeroAt = kScaleAt + 2 * kScales;
+  static constexpr int kStage = (kZeroAt + 2 * kZeros + 127) / 128 * 128;
+  static constexpr int kQ = D * RT * 2;                                // Q in fragment order
+  static constexpr int kSmall = RT * (NG + 3 + 2 * kAttnWarps) * 4 + 128;
+  static constexpr int kBudget = 227 * 1024 / kBlocks - 1024 - kQ - kSmall;
+  static constexpr int kFit = kBudget / (kAttnWarps * kStage);
+  static constexpr int kStages = kFit < 2 ? 2 : (kFit > 4 ? 4 : kFit);
+  static constexpr int kMergePitch = D + 4;                            // floats of a row
+  static constexpr int kMerge = kAttnWarps * 8 * kMergePitch * 4;
+  static constexpr int kRing = kAttnWarps * kStages * kStage;
+  static constexpr int kRingBytes = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kSmem = kRingBytes + kQ + kSmall;
+  static constexpr bool kQInRegs = D * NT <= 256;
+};
+
+namespace attn {
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// (w ^ flip) & mask in one operation.
+template <bool ASYM>
+__device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask) {
+  if (ASYM) return w & mask;
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x28;" : "=r"(r) : "r"(w), "r"(0x88888888u), "r"(mask));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+// 16-byte chunk c of token row r in a tile: permuted so that the 8 rows of
+// an ldmatrix fall into different banks.
+template <int RB>
+__device__ __forceinline__ int chunk_of(int r, int c) {
+  if (RB == 128) return c ^ (r & 7);
+  if (RB == 64) return c ^ ((r >> 1) & 3);
+  if (RB == 32) return c ^ ((r >> 2) & 1);
+  return c;  // rows of 48 bytes: 8 of them fall into different banks as they are
+}
+
+}  // namespace attn
+
+template <typename T, class C>
+__global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
+    attention_mma_kernel(const __grid_constant__ AttentionArgs a, const AttentionSpace ws, const int page_shift) {
+  using namespace attn;
+  constexpr int D = C::D, NT = C::NT, RT = C::RT, DB = C::DB, NG = C::NG, RB = C::RB, RC = C::RC;
+  constexpr bool ASYM = C::ASYM;
+  constexpr float kNegInf = -__builtin_huge_valf();
+
+  extern __shared__ __align__(128) uint8_t smem[];
+  const CacheView& cache = a.cache;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* const sq = smem + C::kRingBytes;
+  float* const s_qsum = reinterpret_cast<float*>(sq + C::kQ);  // [NG][RT]
+  float* const s_f = s_qsum + RT * NG;                          // [RT]
+  int* const s_lo = reinterpret_cast<int*>(s_f + RT);           // [RT]
+  int* const s_hi = s_lo + RT;                                  // [RT]
+  float* const s_m = reinterpret_cast<float*>(s_hi + RT);       // [warps][RT]
+  float* const s_l = s_m + kAttnWarps * RT;                     // [warps][RT]
+  __shared__ int64_t s_scan[kAttnWarps];
+  __shared__ int64_t s_off;
+  __shared__ int s_b;
+
+  // ---- This block's share: units [u0, u1) of all, beginning in sequence b.
+  int64_t units = 0, mine = 0, upto = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kAttnThreads) {
+    const int b = b0 + tid;
+    mine = b < a.batch ? head_units(a, b, RT) * cache.heads : 0;
+    upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) s_scan[warp] = upto;
+    __syncthreads();
+    int64_t all = 0;
+    for (int w = 0; w < kAttnWarps; ++w) {
+      if (w < warp) upto += s_scan[w];
+      all += s_scan[w];
+    }
+    upto += units;  // inclusive, over all sequences up to b
+    if (blockIdx.x == 0 && b < a.batch) ws.prefix[b + 1] = upto;
+    units += all;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && tid == 0) ws.prefix[0] = 0;
+  const int64_t active = active_blocks(units, ws.blocks);
+  if (static_cast<int64_t>(blockIdx.x) >= active) return;
+  const int64_t u0 = share_begin(units, active, blockIdx.x);
+  int64_t left = share_begin(units, active, blockIdx.x + 1) - u0;
+  if (a.batch <= kAttnThreads) {
+    if (upto - mine <= u0 && u0 < upto) {
+      s_b = tid;
+      s_off = u0 - (upto - mine);
+    }
+  } else {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kAttnThreads) {
+      const int b = b0 + tid;
+      mine = b < a.batch ? head_units(a, b, RT) * cache.heads : 0;
+      upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      if (lane == 31) s_scan[warp] = upto;
+      __syncthreads();
+      int64_t all = 0;
+      for (int w = 0; w < kAttnWarps; ++w) {
+        if (w < warp) upto += s_scan[w];
+        all += s_scan[w];
+      }
+      upto += before;
+      if (upto - mine <= u0 && u0 < upto) {
+        s_b = b;
+        s_off = u0 - (upto - mine);
+      }
+      before += all;
+      __syncthreads();
+      if (before > u0) break;  // the same for every thread
+    }
+  }
+  __syncthreads();
+
+  // ---- The item in which the share begins.
+  int b = s_b;
+  int64_t first, count;
+  a.queries(b, first, count);
+  int64_t len = a.kv_len(b);
+  int n_rt = row_tiles(a, count, RT);
+  int h, rt = 0, s0;
+  RowTile tile;
+  {
+    const int64_t per_head = head_units(a, b, RT);
+    int64_t off = s_off;
+    h = static_cast<int>(off / per_head);
+    off -= h * per_head;
+    tile.set(a, len, count, 0, RT);
+    while (off >= tile.steps) {
+      off -= tile.steps;
+      tile.set(a, len, count, ++rt, RT);
+    }
+    s0 = static_cast<int>(off);
+  }
+
+  const uint32_t ring = ptx::smem_u32(smem) + warp * C::kStages * C::kStage;
+
+  while (left > 0) {
+    const int n = left < tile.steps - s0 ? static_cast<int>(left) : tile.steps - s0;
+    const int64_t r0 = static_cast<int64_t>(rt) * RT;
+    const int rows = count * a.ratio - r0 < RT ? static_cast<int>(count * a.ratio - r0) : RT;
+
+    // ---- Queries of the tile: fp16 in fragment order, group sums, bounds.
+    for (int r = warp; r < RT; r += kAttnWarps) {
+      float v[DB];
+      const bool live = r < rows;
+      const int64_t i = live ? (r0 + r) / a.ratio : 0;
+      const int hq = h * a.ratio + (live ? static_cast<int>((r0 + r) - i * a.ratio) : 0);
+      const T* qp = static_cast<const T*>(a.q) + (first + i) * a.q_token_stride + hq * a.q_head_stride;
+      float top = 0.0f;
+#pragma unroll
+      for (int c = 0; c < DB; ++c) {
+        v[c] = live ? Elem<T>::load(qp + 32 * c + lane) : 0.0f;
+        top = fmaxf(top, fabsf(v[c]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // top in [2^e, 2^(e+1)); elements are scaled by 2^(14 - e).
+      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+      e = e < -100 ? -100 : e;
+      const float scale = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+      const int nt = r >> 3, gr = r & 7, tl = lane >> 3, el = lane & 7;
+      float sum = 0.0f;
+#pragma unroll
+      for (int c = 0; c < DB; ++c) {
+        const __half x = __float2half_rn(v[c] * scale);
+        const __half y = (el & 1) ? __hmul(x, __float2half_rn(0.0625f)) : x;
+        const int step = (el >> 1) & 1, reg = el & 1, half = el >> 2;
+        const int at = ((((c * 2 + step) * NT + nt) * 32 + gr * 4 + tl) * 2 + reg) * 2 + half;
+        reinterpret_cast<__half*>(sq)[at] = y;
+        sum += __half2float(x);
+        if (c % C::BPG == C::BPG - 1) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane == 0) s_qsum[(c / C::BPG) * RT + r] = -sum * (ASYM ? 0x1p-24f : 0x1p-21f);
+          sum = 0.0f;
+        }
+      }
+      if (lane == 0) {
+        int64_t lo = 0, hi = 0;
+        if (live) a.visible(len - count + i, len, lo, hi);
+        s_lo[r] = static_cast<int>(lo);
+        s_hi[r] = static_cast<int>(hi);
+        s_f[r] = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23) * (a.sm_scale * 1.4426950408889634f);
+      }
+    }
+    __syncthreads();
+    // Tokens that every row of the tile sees.
+    const int all_lo = s_lo[rows - 1], all_hi = s_hi[0];
+
+    uint2 qf[C::kQInRegs ? DB * 2 * NT : 1];
+    if (C::kQInRegs) {
+#pragma unroll
+      for (int i = 0; i < DB * 2 * NT; ++i) qf[i] = reinterpret_cast<const uint2*>(sq)[i * 32 + lane];
+    }
+    float2 f[NT];
+    float2 qs1[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f[nt] = *reinterpret_cast<const float2*>(s_f + nt * 8 + 2 * t);
+      qs1[nt] = *reinterpret_cast<const float2*>(s_qsum + nt * 8 + 2 * t);
+    }
+
+    float o[DB][2][NT][4], zo[NG][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < DB; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[c][k >> 2][nt][k & 3] = 0.0f;
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) zo[gi][nt][k] = 0.0f;
+      m[nt][0] = m[nt][1] = kNegInf;
+      l[nt][0] = l[nt][1] = 0.0f;
+    }
+    int e_run = 1;  // exponent field of the largest value scale so far
+
+    // ---- Copies: page ids 16 tiles at a time, a lane per block of 16 tokens.
+    const int tile_base = tile.lo + s0 * kAttnStep + warp * kAttnTokens;
+    int page_ids = -1;
+    uint32_t live_blocks = 0u;  // two bits a stage
+    auto issue = [&](int k, int stage) {
+      if (k < n) {
+        if ((k & 15) == 0) {
+          const int tok = tile_base + (k + (lane >> 1)) * kAttnStep + (lane & 1) * 16;
+          page_ids = -1;
+          if (tok < tile.hi) {
+            const int id = __ldg(a.page_table + b * a.table_stride + (tok >> page_shift));
+            page_ids = id >= 0 && id < cache.pages ? id : -1;
+          }
+        }
+        const int tok0 = tile_base + k * kAttnStep;
+        const int id0 = __shfl_sync(0xffffffffu, page_ids, (k & 15) * 2);
+        const int id1 = __shfl_sync(0xffffffffu, page_ids, (k & 15) * 2 + 1);
+        const int mask = cache.page_size - 1;
+        // Rows of the two blocks' first tokens, keys; values lie `vrows` on.
+        const int64_t row0 = cache.row(id0, 0, h, tok0 & mask);
+        const int64_t row1 = cache.row(id1, 0, h, (tok0 + 16) & mask);
+        const int64_t vrows = static_cast<int64_t>(cache.heads) << page_shift;
+        const uint32_t dst = ring + stage * C::kStage;
+#pragma unroll
+        for (int i = 0; i < 2 * RC; ++i) {
+          const int q = i * 32 + lane;
+          const int r = q / RC, c = q % RC;
+          const bool second = r >= 16;
+          if ((second ? id1 : id0) >= 0) {
+            const uint8_t* src =
+                cache.packed + ((second ? row1 - 16 : row0) + r) * RB + c * 16;
+            const uint32_t at = dst + r * RB + chunk_of<RB>(r, c) * 16;
+            cp16(at, src);
+            cp16(at + C::kCodes, src + vrows * RB);
+          }
+        }
+        // Scales: a block's 16 NG halves are 2 NG chunks, keys then values.
+#pragma unroll
+        for (int i0 = 0; i0 < 8 * NG; i0 += 32) {
+          const int i = i0 + lane;
+          const int kv = i / (4 * NG), blk = (i / (2 * NG)) & 1, c = i % (2 * NG);
+          if (i < 8 * NG && (blk ? id1 : id0) >= 0)
+            cp16(dst + C::kScaleAt + kv * C::kScales + blk * 32 * NG + c * 16,
+                 cache.scales + ((blk ? row1 : row0) + kv * vrows) * NG + c * 8);
+        }
+        if (ASYM) {
+#pragma unroll
+          for (int i0 = 0; i0 < 4 * NG; i0 += 32) {
+            const int i = i0 + lane;
+            const int kv = i / (2 * NG), blk = (i / NG) & 1, c = i % NG;
+            if (i < 4 * NG && (blk ? id1 : id0) >= 0)
+              cp16(dst + C::kZeroAt + kv * C::kZeros + blk * 16 * NG + c * 16,
+                   cache.zeros + ((blk ? row1 : row0) + kv * vrows) * NG + c * 16);
+          }
+        }
+        const uint32_t live = (id0 >= 0 ? 1u : 0u) | (id1 >= 0 ? 2u : 0u);
+        live_blocks = (live_blocks & ~(3u << (2 * stage))) | (live << (2 * stage));
+      }
+      cp_commit();
+    };
+
+#pragma unroll
+    for (int k = 0; k < C::kStages - 1; ++k) issue(k, k);
+    int stage = 0;
+    for (int k = 0; k < n; ++k) {
+      cp_wait<C::kStages - 2>();
+      __syncwarp();
+      issue(k + C::kStages - 1, stage == 0 ? C::kStages - 1 : stage - 1);
+      const uint32_t st = ring + stage * C::kStage;
+      const uint32_t live = (live_blocks >> (2 * stage)) & 3u;
+      stage = stage == C::kStages - 1 ? 0 : stage + 1;
+      const int base = tile_base + k * kAttnStep;
+      if (live == 0u) continue;  // past the end, or no page: the warp has no tokens here
+
+      // ---- S^T = K Q^T for two blocks of 16 tokens.
+      float s[2][NT][4];
+      {
+        float acc[2][NT][4];
+#pragma unroll
+        for (int c = 0; c < DB; ++c) {
+          const int gi = c / C::BPG;
+          if (c % C::BPG == 0) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float2 init = make_float2(0.0f, 0.0f);
+              if (!ASYM)
+                init = NG == 1 ? qs1[nt] : *reinterpret_cast<const float2*>(s_qsum + gi * RT + nt * 8 + 2 * t);
+#pragma unroll
+              for (int mb = 0; mb < 2; ++mb) {
+                acc[mb][nt][0] = acc[mb][nt][2] = init.x;
+                acc[mb][nt][1] = acc[mb][nt][3] = init.y;
+              }
+            }
+          }
+          uint32_t kr[4];
+          ldsm4(st + lane * RB + chunk_of<RB>(lane, c) * 16, kr);
+#pragma unroll
+          for (int step = 0; step < 2; ++step) {
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              lo[i] = pick<ASYM>(kr[i], 0x000F000Fu);
+              hi[i] = pick<ASYM>(kr[i], 0x00F000F0u);
+              kr[i] >>= 8;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int at = (c * 2 + step) * NT + nt;
+              const uint2 q2 = C::kQInRegs ? qf[C::kQInRegs ? at : 0]
+                                           : ptx::lds64(ptx::smem_u32(sq) + (at * 32 + lane) * 8);
+              mma(acc[0][nt], lo[0], lo[1], hi[0], hi[1], q2.x, q2.y);
+              mma(acc[1][nt], lo[2], lo[3], hi[2], hi[3], q2.x, q2.y);
+            }
+          }
+          if (c % C::BPG == C::BPG - 1) {
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const int tok = mb * 16 + half * 8 + g;
+                const float ks =
+                    f16_bits_to_float(lds_u16(st + C::kScaleAt + (tok * NG + gi) * 2)) * 0x1p24f;
+                const float kz =
+                    ASYM ? static_cast<float>(lds_u8(st + C::kZeroAt + tok * NG + gi)) : 0.0f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  float2 qz = make_float2(0.0f, 0.0f);
+                  if (ASYM)
+                    qz = NG == 1 ? qs1[nt]
+                                 : *reinterpret_cast<const float2*>(s_qsum + gi * RT + nt * 8 + 2 * t);
+                  float x0 = acc[mb][nt][2 * half], x1 = acc[mb][nt][2 * half + 1];
+                  if (ASYM) {
+                    x0 = fmaf(kz, qz.x, x0);
+                    x1 = fmaf(kz, qz.y, x1);
+                  }
+                  s[mb][nt][2 * half] = gi == 0 ? ks * x0 : fmaf(ks, x0, s[mb][nt][2 * half]);
+                  s[mb][nt][2 * half + 1] = gi == 0 ? ks * x1 : fmaf(ks, x1, s[mb][nt][2 * half + 1]);
+                }
+              }
+          }
+        }
+      }
+      // Value scales of this lane's tokens, as fp16 bits.
+      uint32_t vs[2][2][NG];
+#pragma unroll
+      for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi)
+            vs[mb][half][gi] =
+                lds_u16(st + C::kScaleAt + C::kScales + ((mb * 16 + half * 8 + g) * NG + gi) * 2);
+#pragma unroll
+      for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[mb][nt][j] *= (j & 1) ? f[nt].y : f[nt].x;
+      // ---- Mask, where some row does not see every token of the tile.
+      if (base < all_lo || base + kAttnTokens > all_hi || live != 3u) {
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int tok = base + mb * 16 + half * 8 + g;
+            const bool here = ((live >> mb) & 1u) != 0u && tok < tile.hi;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int r = nt * 8 + 2 * t + j;
+                if (!here || tok < s_lo[r] || tok >= s_hi[r]) s[mb][nt][2 * half + j] = kNegInf;
+              }
+            if (!here) {  // what is stored there, NaN among it, must not count
+#pragma unroll
+              for (int gi = 0; gi < NG; ++gi) vs[mb][half][gi] = 0u;
+            }
+          }
+      }
+      // ---- Running maxima, and the exponent of the largest value scale.
+      uint32_t vtop = 0u;
+#pragma unroll
+      for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi) vtop = max(vtop, vs[mb][half][gi] & 0x7FFFu);
+      const int e_tile = static_cast<int>(__reduce_max_sync(0xffffffffu, vtop) >> 10);
+      const int e_new = max(e_run, e_tile);
+      float mx[NT][2];
+      bool grew = e_new != e_run;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x = fmaxf(fmaxf(s[0][nt][j], s[0][nt][2 + j]), fmaxf(s[1][nt][j], s[1][nt][2 + j]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          mx[nt][j] = fmaxf(m[nt][j], x);
+          grew = grew || mx[nt][j] != m[nt][j];
+        }
+      if (__any_sync(0xffffffffu, grew)) {
+        const float shrink = __uint_as_float(static_cast<uint32_t>(127 + e_run - e_new) << 23);
+        e_run = e_new;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float al[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            al[j] = m[nt][j] == mx[nt][j] ? 1.0f : ex2(m[nt][j] - mx[nt][j]);
+            m[nt][j] = mx[nt][j];
+            l[nt][j] *= al[j];
+            al[j] *= shrink;
+          }
+#pragma unroll
+          for (int c = 0; c < DB; ++c)
+#pragma unroll
+            for (int k2 = 0; k2 < 8; ++k2) o[c][k2 >> 2][nt][k2 & 3] *= al[k2 & 1];
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+            for (int k2 = 0; k2 < 4; ++k2) zo[gi][nt][k2] *= al[k2 & 1];
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float ref = m[nt][j] == kNegInf ? 0.0f : m[nt][j];
+#pragma unroll
+          for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const float p = ex2(s[mb][nt][2 * half + j] - ref);
+              s[mb][nt][2 * half + j] = p;
+              l[nt][j] += p;
+            }
+        }
+      // ---- O^T += V^T W^T, W = P times the value scales, as fp16.
+      const float wf = __uint_as_float(static_cast<uint32_t>(127 + 29 - e_run) << 23);
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int c = 0; c < DB; ++c) {
+        const int gi = c / C::BPG;
+        if (c % C::BPG == 0) {
+#pragma unroll
+          for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const float w = f16_bits_to_float(vs[mb][half][gi]) * wf;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                pb[mb][nt][half] =
+                    transpose8x8(pack_half2(s[mb][nt][2 * half] * w, s[mb][nt][2 * half + 1] * w));
+            }
+#pragma unroll
+          for (int mb = 0; mb < 2; ++mb) {
+            uint32_t z0 = 0x00080008u, z1 = 0x00080008u;
+            if (ASYM) {
+              const uint32_t za = st + C::kZeroAt + C::kZeros + (mb * 16 + 2 * t) * NG + gi;
+              z0 = lds_u8(za) | (lds_u8(za + NG) << 16);
+              z1 = lds_u8(za + 8 * NG) | (lds_u8(za + 9 * NG) << 16);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(zo[gi][nt], z0, z0, z1, z1, pb[mb][nt][0], pb[mb][nt][1]);
+          }
+        }
+        uint32_t vr[4];
+        ldsm4t(st + C::kCodes + lane * RB + chunk_of<RB>(lane, c) * 16, vr);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t lo[4], hi[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            lo[i] = pick<ASYM>(vr[i], 0x000F000Fu);
+            hi[i] = pick<ASYM>(vr[i], 0x00F000F0u);
+            vr[i] >>= 8;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma(o[c][half][nt], lo[0], hi[0], lo[1], hi[1], pb[0][nt][0], pb[0][nt][1]);
+            mma(o[c][half][nt], lo[2], hi[2], lo[3], hi[3], pb[1][nt][0], pb[1][nt][1]);
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+
+    // ---- Join the warps, then store the item's result or the piece's sums.
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int o2 = 4; o2 < 32; o2 <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], o2);
+        if (g == 0) {
+          s_m[warp * RT + nt * 8 + 2 * t + j] = m[nt][j];
+          s_l[warp * RT + nt * 8 + 2 * t + j] = l[nt][j];
+        }
+      }
+    const bool whole = n == tile.steps;
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (s0 == 0 ? 1 : 0);
+    float* const buf = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      __syncthreads();  // tiles read (first time), or the last rows' sums read
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = nt * 8 + 2 * t + j;
+        float top = s_m[r];
+#pragma unroll
+        for (int w = 1; w < kAttnWarps; ++w) top = fmaxf(top, s_m[w * RT + r]);
+        // Codes are 2^-24 times themselves, weights 2^(29 - e_run).
+        const float scale =
+            (m[nt][j] == top ? 1.0f : ex2(m[nt][j] - top)) * __uint_as_float(static_cast<uint32_t>(127 + 24 + e_run - 29) << 23);
+        float* dst = buf + (warp * 8 + 2 * t + j) * C::kMergePitch + 4 * g;
+#pragma unroll
+        for (int c = 0; c < DB; ++c) {
+          const float z = zo[c / C::BPG][nt][j];
+          float4 v;
+          v.x = (o[c][0][nt][j] - z) * scale;
+          v.y = (o[c][0][nt][2 + j] * 0.0625f - z) * scale;
+          v.z = (o[c][1][nt][j] - z) * scale;
+          v.w = (o[c][1][nt][2 + j] * 0.0625f - z) * scale;
+          *reinterpret_cast<float4*>(dst + 32 * c) = v;
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < 8 * (D / 4); i += kAttnThreads) {
+        const int rr = i / (D / 4), d = (i % (D / 4)) * 4;
+        const int r = nt * 8 + rr;
+        if (r >= rows) continue;
+        float4 v = *reinterpret_cast<const float4*>(buf + rr * C::kMergePitch + d);
+        float top = s_m[r];
+#pragma unroll
+        for (int w = 1; w < kAttnWarps; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(buf + (w * 8 + rr) * C::kMergePitch + d);
+          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+          top = fmaxf(top, s_m[w * RT + r]);
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+          const float mw = s_m[w * RT + r];
+          sum += s_l[w * RT + r] * (mw == top ? 1.0f : ex2(mw - top));
+        }
+        if (whole) {
+          const int64_t i_tok = (r0 + r) / a.ratio;
+          const int64_t at = (first + i_tok) * a.q_heads + h * a.ratio + ((r0 + r) - i_tok * a.ratio);
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          T* out = static_cast<T*>(a.out) + at * D + d;
+          alignas(8) T four[4];
+          store_as(four, v.x * inv);
+          store_as(four + 1, v.y * inv);
+          store_as(four + 2, v.z * inv);
+          store_as(four + 3, v.w * inv);
+          *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(four);
+          if (d == 0 && a.lse != nullptr)
+            a.lse[at] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
+        } else {
+          *reinterpret_cast<float4*>(ws.o + (slot * RT + r) * D + d) = v;
+          if (d == 0) {
+            ws.ml[(slot * RT + r) * 2] = top;
+            ws.ml[(slot * RT + r) * 2 + 1] = sum;
+          }
+        }
+      }
+    }
+    __syncthreads();
+
+    // ---- The next item.
+    left -= n;
+    if (left == 0) break;
+    s0 = 0;
+    do {
+      if (++rt == n_rt) {
+        rt = 0;
+        if (++h == cache.heads) {
+          h = 0;
+          do {
+            ++b;
+            a.queries(b, first, count);
+            len = a.kv_len(b);
+            n_rt = row_tiles(a, count, RT);
+          } while (n_rt == 0);
+        }
+      }
+      tile.set(a, len, count, rt, RT);
+    } while (tile.steps == 0);
+  }
+  ptx::launch_dependents();
+}
+
+// Joins the pieces of split items and writes the rows that see nothing.  A
+// query row of one head is given to `wpr` of the block's warps (1 when there
+// are rows enough to fill the GPU, else all of them), a share of the pieces
+// to each.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    attention_join_kernel(const __grid_constant__ AttentionArgs a, const AttentionSpace ws, const int RT, const int wpr) {
+  constexpr float kNegInf = -__builtin_huge_valf();
+  __shared__ float part[8][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int D = a.cache.head_dim;
+  const int64_t index = static_cast<int64_t>(blockIdx.x) * (8 / wpr) + warp / wpr;
+  const int64_t tok = index / a.q_heads;
+  const int hq = static_cast<int>(index - tok * a.q_heads);
+  int b = -1;
+  if (tok < a.rows) b = a.sequence_of(tok);
+  int64_t first = 0, count = 0, r = 0, before = 0, per_head = 0, p_end = 0, p0 = 0;
+  int steps = 0, rt = 0;
+  if (b >= 0) {
+    a.queries(b, first, count);
+    const int64_t len = a.kv_len(b);
+    r = (tok - first) * a.ratio + hq % a.ratio;
+    rt = static_cast<int>(r / RT);
+    const int n = row_tiles(a, count, RT);
+    for (int i = 0; i < n; ++i) {
+      RowTile tile;
+      tile.set(a, len, count, i, RT);
+      if (i < rt) before += tile.steps;
+      if (i == rt) steps = tile.steps;
+      per_head += tile.steps;
+    }
+  }
+  ptx::grid_dependency_wait();
+  int64_t active = 1;
+  if (steps > 0) {
+    const int64_t units = ws.prefix[a.batch];
+    active = active_blocks(units, ws.blocks);
+    const int64_t begin = ws.prefix[b] + (hq / a.ratio) * per_head + before;
+    p0 = share_of(units, active, begin);
+    p_end = share_of(units, active, begin + steps - 1) + 1;
+  }
+  const bool join = p_end - p0 > 1;
+  const bool empty = b >= 0 && steps == 0;
+  float4 v[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  float top = kNegInf, sum = 0.0f;
+  const int rr = static_cast<int>(r - static_cast<int64_t>(rt) * RT);
+  if (join) {
+    // The first piece ends its block's share, every other one begins its own.
+    auto slot = [&](int64_t p) { return (2 * p + (p == p0 ? 1 : 0)) * RT + rr; };
+    for (int64_t p = p0 + lane; p < p_end; p += 32) top = fmaxf(top, ws.ml[slot(p) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int64_t p = p0 + lane; p < p_end; p += 32) {
+      const float mp = ws.ml[slot(p) * 2];
+      sum += ws.ml[slot(p) * 2 + 1] * (mp == top ? 1.0f : attn::ex2(mp - top));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll 4
+    for (int64_t p = p0 + warp % wpr; p < p_end; p += wpr) {
+      const int64_t s = slot(p);
+      const float mp = ws.ml[s * 2];
+      const float w = mp == top ? 1.0f : attn::ex2(mp - top);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int d = i * 128 + lane * 4;
+        if (d < D) {
+          const float4 x = *reinterpret_cast<const float4*>(ws.o + s * D + d);
+          v[i].x = fmaf(w, x.x, v[i].x);
+          v[i].y = fmaf(w, x.y, v[i].y);
+          v[i].z = fmaf(w, x.z, v[i].z);
+          v[i].w = fmaf(w, x.w, v[i].w);
+        }
+      }
+    }
+  }
+  if (wpr > 1) {  // one row a block: join is the same for all its threads
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int d = i * 128 + lane * 4;
+      *reinterpret_cast<float4*>(&part[warp][d]) = v[i];
+    }
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int d = i * 128 + lane * 4;
+      for (int w = 1; w < 8; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(&part[w][d]);
+        v[i].x += x.x; v[i].y += x.y; v[i].z += x.z; v[i].w += x.w;
+      }
+    }
+  }
+  if (!join && !empty) return;
+  const int64_t at = tok * a.q_heads + hq;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int d = i * 128 + lane * 4;
+    if (d < D) {
+      alignas(8) T four[4];
+      store_as(four, v[i].x * inv);
+      store_as(four + 1, v[i].y * inv);
+      store_as(four + 2, v[i].z * inv);
+      store_as(four + 3, v[i].w * inv);
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * D + d) = *reinterpret_cast<const uint2*>(four);
+    }
+  }
+  if (lane == 0 && a.lse != nullptr)
+    a.lse[at] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// ---- Host side ------------------------------------------------------------
+
+// Query rows of a tile: the smallest of 8, 16 and 32 that holds the rows of an
+// average sequence (query tokens times ratio); 16 at most for 256 elements,
+// where the accumulators of 32 rows do not fit in registers.
+inline int attention_row_tile(int head_dim, int64_t rows, int64_t batch, int ratio) {
+  const int64_t r = (rows * ratio + batch - 1) / batch;
+  if (r <= 8) return 8;
+  return r <= 16 || head_dim > 128 ? 16 : 32;
+}
+
+template <class C>
+int attention_blocks() {
+  return num_sms() * C::kBlocks;
+}
+
+template <typename T, class C>
+cudaError_t launch_attention_cfg(const AttentionArgs& a, void* workspace, cudaStream_t stream) {
+  AttentionSpace ws;
+  ws.blocks = attention_blocks<C>();
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  ws.prefix = reinterpret_cast<int64_t*>(p);
+  p += attention_prefix_bytes(a.batch);
+  ws.o = reinterpret_cast<float*>(p);
+  ws.ml = ws.o + 2LL * ws.blocks * C::RT * C::D;
+  auto kernel = attention_mma_kernel<T, C>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  int shift = 0;
+  while ((1 << shift) < a.cache.page_size) ++shift;
+  kernel<<<ws.blocks, kAttnThreads, C::kSmem, stream>>>(a, ws, shift);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // The join starts while the last shares are finished.
+  const int64_t rows = a.rows * a.q_heads;
+  const int wpr = rows <= 2048 ? 8 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(wpr == 8 ? rows : (rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T>, a, ws, C::RT, wpr);
+}
+
+// Calls f with the configuration for a cache and row tile; false if none.
+template <int D, int GROUP, class F>
+bool with_attention_cfg(bool asym, int rt, F&& f) {
+  if (rt == 8) {
+    if (asym) f(AttnCfg<D, GROUP, 1, true>{}); else f(AttnCfg<D, GROUP, 1, false>{});
+    return true;
+  }
+  if (rt == 16) {
+    if (asym) f(AttnCfg<D, GROUP, 2, true>{}); else f(AttnCfg<D, GROUP, 2, false>{});
+    return true;
+  }
+  if constexpr (D <= 128) {
+    if (rt == 32) {
+      if (asym) f(AttnCfg<D, GROUP, 4, true>{}); else f(AttnCfg<D, GROUP, 4, false>{});
+      return true;
+    }
+  }
+  return false;
+}
+
+}  // namespace int4lib

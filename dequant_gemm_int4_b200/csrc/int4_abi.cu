@@ -3,11 +3,13 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
 #include <cstdio>
 #include <mutex>
 #include <string>
 
 #include "int4.h"
+#include "cache.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -356,6 +358,174 @@ int int4_matmul_select(int32_t x_dtype, int64_t K, int32_t group, int64_t M, int
   // Alignment of real buffers is not known here; assume allocator alignment.
   static const uint8_t* const kAligned = reinterpret_cast<const uint8_t*>(static_cast<uintptr_t>(256));
   return matmul_choose(static_cast<DType>(x_dtype), K, group, M, N, kAligned, kAligned);
+}
+
+// ---- The 4-bit key/value cache --------------------------------------------------
+
+static int cache_check(const char* name, const int4_cache* c, int32_t dtype, int4lib::CacheView* view) {
+  char msg[200];
+  if (c == nullptr) {
+    std::snprintf(msg, sizeof msg, "%s: null cache", name);
+    return int4lib::fail(INT4_ERR_ARG, msg);
+  }
+  if (!int4lib::dtype_ok(dtype)) {
+    std::snprintf(msg, sizeof msg, "%s: unknown dtype", name);
+    return int4lib::fail(INT4_ERR_DTYPE, msg);
+  }
+  if (c->pages < 0 || c->page_size < 1 || c->heads < 1 || c->head_dim < 1 || c->head_dim > 512 ||
+      c->group < 1) {
+    std::snprintf(msg, sizeof msg,
+                  "%s: need pages >= 0, page_size, heads, group >= 1 and head_dim in [1, 512]", name);
+    return int4lib::fail(INT4_ERR_ARG, msg);
+  }
+  const int64_t rows = 2 * static_cast<int64_t>(c->heads) * c->page_size;  // below 2^63
+  if (!int4lib::mul_ok(rows, c->pages) || !int4lib::mul_ok(rows * (c->pages > 0 ? c->pages : 1), 512)) {
+    std::snprintf(msg, sizeof msg, "%s: cache too large", name);
+    return int4lib::fail(INT4_ERR_ARG, msg);
+  }
+  if (c->pages > 0 && (!c->packed || !c->scales)) {
+    std::snprintf(msg, sizeof msg, "%s: null packed or scales", name);
+    return int4lib::fail(INT4_ERR_ARG, msg);
+  }
+  if (!int4lib::aligned(c->scales, 2)) {
+    std::snprintf(msg, sizeof msg, "%s: scales not 2-byte aligned", name);
+    return int4lib::fail(INT4_ERR_ALIGN, msg);
+  }
+  const int32_t group = c->group < c->head_dim ? c->group : c->head_dim;
+  *view = {static_cast<uint8_t*>(c->packed), static_cast<uint16_t*>(c->scales),
+           static_cast<uint8_t*>(c->zeros), c->pages, c->page_size, c->heads, c->head_dim, group,
+           (c->head_dim + 1) / 2, (c->head_dim + group - 1) / group};
+  return INT4_OK;
+}
+
+int int4_cache_write(const int4_cache* cache, const void* k, int64_t k_token_stride,
+                     int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                     int64_t v_head_stride, int32_t dtype, int64_t tokens, const int64_t* slots,
+                     void* stream) {
+  int4lib::CacheView view;
+  const int rc = cache_check("int4_cache_write", cache, dtype, &view);
+  if (rc != INT4_OK) return rc;
+  if (tokens < 0 || !int4lib::mul_ok(tokens, 2 * static_cast<int64_t>(view.heads) * view.head_dim))
+    return int4lib::fail(INT4_ERR_ARG, "int4_cache_write: need tokens >= 0, and sizes below 2^62");
+  if (tokens == 0 || view.pages == 0) return INT4_OK;
+  if (!k || !v || !slots) return int4lib::fail(INT4_ERR_ARG, "int4_cache_write: null pointer");
+  const DType t = static_cast<DType>(dtype);
+  const size_t elt = int4lib::dtype_size(t);
+  if (!int4lib::aligned(k, elt) || !int4lib::aligned(v, elt) || !int4lib::aligned(slots, 8))
+    return int4lib::fail(INT4_ERR_ALIGN, "int4_cache_write: k, v or slots not aligned to its element size");
+  const cudaError_t e =
+      int4lib::launch_cache_write(view, k, v, t, tokens, {k_token_stride, v_token_stride},
+                                  {k_head_stride, v_head_stride}, slots, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? INT4_OK : int4lib::fail_cuda(e, "int4_cache_write");
+}
+
+int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
+                    int32_t dtype, void* stream) {
+  int4lib::CacheView view;
+  const int rc = cache_check("int4_cache_read", cache, dtype, &view);
+  if (rc != INT4_OK) return rc;
+  if (tokens < 0 || !int4lib::mul_ok(tokens, 2 * static_cast<int64_t>(view.heads) * view.head_dim))
+    return int4lib::fail(INT4_ERR_ARG, "int4_cache_read: need tokens >= 0, and sizes below 2^62");
+  if (tokens == 0) return INT4_OK;
+  if (!k || !v || !slots) return int4lib::fail(INT4_ERR_ARG, "int4_cache_read: null pointer");
+  const DType t = static_cast<DType>(dtype);
+  const size_t elt = int4lib::dtype_size(t);
+  if (!int4lib::aligned(k, elt) || !int4lib::aligned(v, elt) || !int4lib::aligned(slots, 8))
+    return int4lib::fail(INT4_ERR_ALIGN, "int4_cache_read: k, v or slots not aligned to its element size");
+  const cudaError_t e =
+      int4lib::launch_cache_read(view, slots, tokens, k, v, t, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? INT4_OK : int4lib::fail_cuda(e, "int4_cache_read");
+}
+
+// The sizes of an attention call, and the kernel that takes it.
+static int attention_plan(const char* name, const int4lib::CacheView& view, DType t, int64_t rows,
+                          int32_t q_heads, int32_t batch, int32_t max_pages, const void* out,
+                          int32_t path, bool* mma, size_t* bytes) {
+  char msg[200];
+  *bytes = 0;
+  if (rows < 0 || q_heads < 1 || q_heads % view.heads != 0 || batch < 0 || max_pages < 0 ||
+      !int4lib::mul_ok(rows, static_cast<int64_t>(q_heads) * view.head_dim) ||
+      rows * static_cast<int64_t>(q_heads) > 0x7FFFFFFF) {
+    std::snprintf(msg, sizeof msg,
+                  "%s: need rows, batch, max_pages >= 0, q_heads a multiple of heads and "
+                  "rows * q_heads below 2^31",
+                  name);
+    return int4lib::fail(INT4_ERR_ARG, msg);
+  }
+  *mma = int4lib::cache_attention_mma_supported(view, t, out, max_pages);
+  if (path == INT4_PATH_DECODE && !*mma) {
+    std::snprintf(msg, sizeof msg, "%s: the tensor-core kernels cannot run this call", name);
+    return int4lib::fail(INT4_ERR_UNSUPPORTED, msg);
+  }
+  if (path != INT4_PATH_AUTO && path != INT4_PATH_SIMT && path != INT4_PATH_DECODE) {
+    std::snprintf(msg, sizeof msg, "%s: unknown path", name);
+    return int4lib::fail(INT4_ERR_ARG, msg);
+  }
+  if (path == INT4_PATH_SIMT) *mma = false;
+  if (*mma && rows > 0 && batch > 0)
+    *bytes = int4lib::cache_attention_mma_workspace(view, rows, batch, q_heads / view.heads);
+  return INT4_OK;
+}
+
+int int4_cache_attention_workspace_size(const int4_cache* cache, int32_t dtype, int64_t rows,
+                                        int32_t q_heads, int32_t batch, int32_t max_pages,
+                                        int32_t path, size_t* bytes) {
+  const char* name = "int4_cache_attention_workspace_size";
+  if (bytes == nullptr) return int4lib::fail(INT4_ERR_ARG, "int4_cache_attention_workspace_size: null output");
+  *bytes = 0;
+  int4lib::CacheView view;
+  const int rc = cache_check(name, cache, dtype, &view);
+  if (rc != INT4_OK) return rc;
+  bool mma;
+  return attention_plan(name, view, static_cast<DType>(dtype), rows, q_heads, batch, max_pages, nullptr,
+                        path, &mma, bytes);
+}
+
+int int4_cache_attention(const int4_cache* cache, const void* q, int64_t q_token_stride,
+                         int64_t q_head_stride, int32_t dtype, int64_t rows, int32_t q_heads,
+                         const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                         const int32_t* kv_lens, const int32_t* q_starts, int32_t batch,
+                         int32_t causal, int32_t window, float sm_scale, void* out, float* lse,
+                         int32_t path, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* name = "int4_cache_attention";
+  int4lib::CacheView view;
+  const int rc = cache_check(name, cache, dtype, &view);
+  if (rc != INT4_OK) return rc;
+  const DType t = static_cast<DType>(dtype);
+  bool mma;
+  size_t need;
+  const int rp = attention_plan(name, view, t, rows, q_heads, batch, max_pages, out, path, &mma, &need);
+  if (rp != INT4_OK) return rp;
+  if (window < 0 || !std::isfinite(sm_scale))
+    return int4lib::fail(INT4_ERR_ARG, "int4_cache_attention: need window >= 0 and a finite sm_scale");
+  if (rows == 0 || batch == 0) return INT4_OK;
+  if (q_starts == nullptr && rows % batch != 0)
+    return int4lib::fail(INT4_ERR_ARG, "int4_cache_attention: without q_starts, batch must divide rows");
+  if (!q || !out || !kv_lens || (max_pages > 0 && !page_table))
+    return int4lib::fail(INT4_ERR_ARG, "int4_cache_attention: null pointer");
+  const size_t elt = int4lib::dtype_size(t);
+  if (!int4lib::aligned(q, elt) || !int4lib::aligned(out, elt) || !int4lib::aligned(page_table, 4) ||
+      !int4lib::aligned(kv_lens, 4) || !int4lib::aligned(q_starts, 4) || !int4lib::aligned(lse, 4))
+    return int4lib::fail(INT4_ERR_ALIGN, "int4_cache_attention: a pointer is not aligned to its element size");
+  if (workspace == nullptr && workspace_bytes != 0)
+    return int4lib::fail(INT4_ERR_ARG, "int4_cache_attention: null workspace with a non-zero size");
+  if (!int4lib::aligned(workspace, 256))
+    return int4lib::fail(INT4_ERR_ALIGN, "int4_cache_attention: workspace not 256-byte aligned");
+  if (workspace_bytes < need) {
+    char msg[200];
+    std::snprintf(msg, sizeof msg,
+                  "int4_cache_attention: this call needs a workspace of %zu bytes, %zu given "
+                  "(int4_cache_attention_workspace_size)",
+                  need, workspace_bytes);
+    return int4lib::fail(INT4_ERR_ARG, msg);
+  }
+  const int4lib::AttentionArgs a = {view, q, q_token_stride, q_head_stride, out, lse, page_table,
+                                    table_stride, kv_lens, q_starts, rows, batch, max_pages, q_heads,
+                                    q_heads / view.heads, causal != 0 ? 1 : 0, window, sm_scale};
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = mma ? int4lib::launch_cache_attention_mma(a, t, workspace, s)
+                            : int4lib::launch_cache_attention_any(a, t, s);
+  return e == cudaSuccess ? INT4_OK : int4lib::fail_cuda(e, name);
 }
 
 int int4_device_status(void* stream) {

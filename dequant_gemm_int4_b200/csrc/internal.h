@@ -83,6 +83,33 @@ cudaError_t launch_matmul_prefill(const void* x, DType xt, const uint8_t* packed
 size_t prefill_workspace_size(int64_t K, int group, int64_t M, int64_t N);
 constexpr size_t kWorkspaceCounterBytes = 4096;
 
+// cache_write.cu: the 4-bit key/value cache (cache.cuh).  Strides in elements,
+// of k and of v.
+struct CacheView;
+struct AttentionArgs;
+cudaError_t launch_cache_write(const CacheView& cache, const void* k, const void* v, DType t,
+                               int64_t tokens, const int64_t (&token_stride)[2],
+                               const int64_t (&head_stride)[2], const int64_t* slots,
+                               cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheView& cache, const int64_t* slots, int64_t tokens, void* k,
+                              void* v, DType t, cudaStream_t stream);
+// cache_attention.cu: any shape, and the tensor-core kernels with their
+// workspace (any content).
+cudaError_t launch_cache_attention_any(const AttentionArgs& a, DType t, cudaStream_t stream);
+bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out, int64_t max_pages);
+size_t cache_attention_mma_workspace(const CacheView& c, int64_t rows, int64_t batch, int ratio);
+cudaError_t launch_cache_attention_mma(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
+// cache_attention_<D>.cu: the kernels for heads of D elements; rt: query rows
+// of a tile.
+cudaError_t launch_cache_attention_64(const AttentionArgs& a, DType t, int rt, void* workspace, cudaStream_t stream);
+cudaError_t launch_cache_attention_96(const AttentionArgs& a, DType t, int rt, void* workspace, cudaStream_t stream);
+cudaError_t launch_cache_attention_128(const AttentionArgs& a, DType t, int rt, void* workspace, cudaStream_t stream);
+cudaError_t launch_cache_attention_256(const AttentionArgs& a, DType t, int rt, void* workspace, cudaStream_t stream);
+int cache_attention_blocks_64(int group, bool asym, int rt);
+int cache_attention_blocks_96(int group, bool asym, int rt);
+int cache_attention_blocks_128(int group, bool asym, int rt);
+int cache_attention_blocks_256(int group, bool asym, int rt);
+
 int num_sms();  // SM count of the current device (cached per device)
 
 // Grid of at most one resident wave of `kern` (256-thread blocks, no dynamic

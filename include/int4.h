@@ -328,6 +328,140 @@ int int4_matmul_decode_noalloc(const void* x, int32_t x_dtype, const uint8_t* pa
 int int4_matmul_select(int32_t x_dtype, int64_t K, int32_t group, int64_t M, int64_t N);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The 4-bit key/value cache: the other large tensor of decoding, in the codes
+ * of the weights.  The pages have no counterpart; the schemes are theirs.
+ * ---------------------------------------------------------------------------
+ *
+ * int4_cache - a paged cache of keys and values, and its sizes.
+ *
+ *   packed [pages, 2, heads, page_size, ceil(head_dim / 2)] uint8
+ *   scales [pages, 2, heads, page_size, G] fp16 bits, G = ceil(head_dim / group)
+ *   zeros  [pages, 2, heads, page_size, G] uint8, or NULL: the symmetric scheme
+ *
+ * dense, keys at index 0 and values at index 1 of the second dimension.  Token
+ * `slot` lies in page slot / page_size at offset slot % page_size.  Its row of
+ * one head is coded bit for bit as int4_quantize codes a row of K = head_dim
+ * weights (zeros == NULL), or int4_quantize_affine (zeros given).
+ *
+ * pages >= 0; page_size, heads, head_dim, group >= 1; head_dim <= 512.
+ * Alignment: scales 2 bytes; packed and zeros any.  Every entry below accepts
+ * every such cache; the fast kernels take packed, scales and zeros 16-byte
+ * aligned.
+ */
+typedef struct {
+  void* packed;
+  void* scales;
+  void* zeros;
+  int64_t pages;
+  int32_t page_size;
+  int32_t heads;
+  int32_t head_dim;
+  int32_t group;
+} int4_cache;
+
+/*
+ * int4_cache_write - quantize the keys and values of new tokens into their
+ * slots.
+ *
+ * k, v     [tokens, heads, head_dim] device inputs of `dtype`, aligned to their
+ *          element size; element d of head h of token t lies at
+ *          t * token_stride + h * head_stride + d (strides in elements, any
+ *          sign), so both may lie inside the rows of a fused projection.
+ * slots    [tokens] int64 device input, 8-byte aligned.  A token whose slot is
+ *          negative or at least pages * page_size (padding) is not written.
+ *          The other slots must be distinct: two tokens in one slot race.
+ * Bit-exact.  Precondition: k and v are finite (else unspecified codes).
+ */
+int int4_cache_write(const int4_cache* cache, const void* k, int64_t k_token_stride,
+                     int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                     int64_t v_head_stride, int32_t dtype, int64_t tokens, const int64_t* slots,
+                     void* stream);
+
+/*
+ * int4_cache_read - the keys and values of given slots, dequantized.
+ *
+ * k, v     [tokens, heads, head_dim] dense device outputs of `dtype`, aligned
+ *          to their element size: q s, or (q - z) s, rounded once, to nearest
+ *          even (int4_dequantize's rule).  Bit-exact.  A token whose slot is
+ *          negative or at least pages * page_size reads as zeros.
+ * slots    [tokens] int64 device input, 8-byte aligned; a slot may occur
+ *          several times.
+ */
+int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
+                    int32_t dtype, void* stream);
+
+/*
+ * int4_cache_attention - queries attend over the cached tokens of their
+ * sequences.
+ *
+ * Sequence b (0 <= b < batch) has len = kv_lens[b] cached tokens, token j in
+ * page page_table[b][j / page_size] at offset j % page_size, and the query
+ * rows t in [q_starts[b], q_starts[b + 1]) (q_starts == NULL: rows / batch
+ * each).  Its last query stands at its last token: the i-th of n queries at
+ * position p = len - n + i.  It sees the tokens j with 0 <= j < len,
+ * j <= p if `causal`, and j > p - window if window > 0.  Query head hq reads
+ * the keys and values of head hq / (q_heads / heads).  With K, V the values of
+ * int4_cache_read in fp32:
+ *   S_j = sm_scale * sum_d q[t, hq, d] K[j, d]
+ *   lse[t, hq] = log sum_j exp(S_j)
+ *   out[t, hq] = sum_j exp(S_j - lse) V[j]
+ * A query that sees no token gets out = 0 and lse = -infinity.  Rows that
+ * belong to no sequence (past q_starts[batch]) are left as they were.
+ *
+ * Never read: tokens that no query sees, and table entries past a sequence's
+ * last token.  Stored NaN or infinity there has no effect.  A table entry that
+ * is negative or at least `pages` holds no tokens (its positions are hidden);
+ * kv_lens below 0 counts as 0, above max_pages * page_size as that.
+ *
+ * q          [rows, q_heads, head_dim] of `dtype`, aligned to its element size;
+ *            strides in elements as for int4_cache_write.
+ * out        [rows, q_heads, head_dim] dense, of `dtype`.
+ * lse        [rows, q_heads] fp32, or NULL.
+ * page_table [batch, max_pages] int32, rows `table_stride` elements apart.
+ * kv_lens    [batch] int32.  q_starts [batch + 1] int32, non-decreasing, within
+ *            [0, rows], or NULL (then batch must divide rows).
+ * sm_scale   finite.
+ *
+ * Accuracy: S, the softmax's maximum and sum, and out's sums are fp32.  For
+ * fp32 q so are the products.  For bf16 and fp16 q the products run on tensor
+ * cores: q and the codes exactly (elements of q below 2^-24 of the row's
+ * largest to 2^-38 of it), the weights exp(S_j) s_j rounded to fp16, 2^-11
+ * relative each.  Deterministic for given sizes, lengths and device.
+ * NaN or infinity in a query makes its own rows NaN.
+ *
+ * `path`: INT4_PATH_AUTO takes the tensor-core kernels (INT4_PATH_DECODE)
+ * where they can run: bf16 or fp16 q, head_dim 64, 96, 128 or 256 in groups of
+ * 32, 64, 128 or head_dim (96: 32 or 96), page_size a power of two from 16 on,
+ * max_pages * page_size <= 2^30, packed, scales and zeros 16-byte and out
+ * 8-byte aligned; else the general kernel (INT4_PATH_SIMT).  A forced path that
+ * cannot run the call returns INT4_ERR_UNSUPPORTED.
+ *
+ * workspace: at least int4_cache_attention_workspace_size bytes (else
+ * INT4_ERR_ARG, nothing launched), 256-byte aligned, of any content; NULL with
+ * workspace_bytes == 0 where that size is 0.  Calls that may overlap in time
+ * need different workspaces, graphs that may be replayed at the same time too.
+ * Nothing else is kept between calls; the lengths, the table and the slots are
+ * read on the device, so a captured call can be replayed with others.
+ */
+int int4_cache_attention(const int4_cache* cache, const void* q, int64_t q_token_stride,
+                         int64_t q_head_stride, int32_t dtype, int64_t rows, int32_t q_heads,
+                         const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                         const int32_t* kv_lens, const int32_t* q_starts, int32_t batch,
+                         int32_t causal, int32_t window, float sm_scale, void* out, float* lse,
+                         int32_t path, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * int4_cache_attention_workspace_size - bytes of workspace that
+ * int4_cache_attention needs on the current device for these sizes (written to
+ * *bytes; 0 for the general kernel).  It depends on the sizes and alignments
+ * in `cache`, not on lengths.  Host-only; launches nothing.
+ */
+int int4_cache_attention_workspace_size(const int4_cache* cache, int32_t dtype, int64_t rows,
+                                        int32_t q_heads, int32_t batch, int32_t max_pages,
+                                        int32_t path, size_t* bytes);
+
+/*
  * int4_device_status - synchronize `stream`, then read and clear the
  * library's device-side status word of the current device.  Returns INT4_OK,
  * or INT4_ERR_TIMEOUT if a kernel's bounded wait on an mbarrier gave up since
