@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
         const int64_t vrows = static_cast<int64_t>(cache.heads) << page_shift;
         const uint32_t dst = ring + stage * C::kStage;
 #pragma unroll
-        for (int i = 0; i < 2 * RC; ++i) {
+        for (int i = 0; i < RC; ++i) {
           const int q = i * 32 + lane;
           const int r = q / RC, c = q % RC;
           const bool second = r >= 16;
@@ -533,8 +533,8 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
                 const int tok = mb * 16 + half * 8 + g;
-                const float ks =
-                    f16_bits_to_float(lds_u16(st + C::kScaleAt + (tok * NG + gi) * 2)) * 0x1p24f;
+                const float k1 = f16_bits_to_float(lds_u16(st + C::kScaleAt + (tok * NG + gi) * 2));
+                const float ks = fmaf(k1, 0x1p24f, k1 * 0.0f);  // an infinite scale gives NaN, as its values do
                 const float kz =
                     ASYM ? static_cast<float>(lds_u8(st + C::kZeroAt + tok * NG + gi)) : 0.0f;
 #pragma unroll
@@ -571,8 +571,12 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[mb][nt][j] *= (j & 1) ? f[nt].y : f[nt].x;
-      // ---- Mask, where some row does not see every token of the tile.
-      if (base < all_lo || base + kAttnTokens > all_hi || live != 3u) {
+      // ---- Mask, where some row does not see every token of the tile; the
+      // largest value scale (of an edge tile's finite ones: what is not seen
+      // must not count, and a row that sees another has no finite output).
+      const bool edge = base < all_lo || base + kAttnTokens > all_hi || live != 3u;
+      uint32_t vtop = 0u;
+      if (edge) {
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
@@ -586,20 +590,22 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
                 const int r = nt * 8 + 2 * t + j;
                 if (!here || tok < s_lo[r] || tok >= s_hi[r]) s[mb][nt][2 * half + j] = kNegInf;
               }
-            if (!here) {  // what is stored there, NaN among it, must not count
 #pragma unroll
-              for (int gi = 0; gi < NG; ++gi) vs[mb][half][gi] = 0u;
+            for (int gi = 0; gi < NG; ++gi) {
+              if (!here) vs[mb][half][gi] = 0u;
+              const uint32_t v = vs[mb][half][gi] & 0x7FFFu;
+              vtop = max(vtop, v < 0x7C00u ? v : 0u);
             }
           }
+      } else {
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) vtop = max(vtop, vs[mb][half][gi] & 0x7FFFu);
       }
       // ---- Running maxima, and the exponent of the largest value scale.
-      uint32_t vtop = 0u;
-#pragma unroll
-      for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int gi = 0; gi < NG; ++gi) vtop = max(vtop, vs[mb][half][gi] & 0x7FFFu);
       const int e_tile = static_cast<int>(__reduce_max_sync(0xffffffffu, vtop) >> 10);
       const int e_new = max(e_run, e_tile);
       float mx[NT][2];
@@ -665,9 +671,14 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
             for (int half = 0; half < 2; ++half) {
               const float w = f16_bits_to_float(vs[mb][half][gi]) * wf;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                pb[mb][nt][half] =
-                    transpose8x8(pack_half2(s[mb][nt][2 * half] * w, s[mb][nt][2 * half + 1] * w));
+              for (int nt = 0; nt < NT; ++nt) {
+                float w0 = s[mb][nt][2 * half] * w, w1 = s[mb][nt][2 * half + 1] * w;
+                if (edge) {  // a hidden token's weight is 0 under any scale
+                  w0 = s[mb][nt][2 * half] == 0.0f ? 0.0f : w0;
+                  w1 = s[mb][nt][2 * half + 1] == 0.0f ? 0.0f : w1;
+                }
+                pb[mb][nt][half] = transpose8x8(pack_half2(w0, w1));
+              }
             }
 #pragma unroll
           for (int mb = 0; mb < 2; ++mb) {

@@ -271,6 +271,24 @@ def test_attention_hidden_places_do_not_count(path):
 
 
 @pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attention_tokens_hidden_from_some_rows(path, bad):
+    """A value scale that is not finite reaches only the rows that see its
+    token, a key scale likewise; the other rows of the tile stay right."""
+    q, packed, scales, zeros, table, lens, group = attention_setup(lens=(70, 45), ratio=2)
+    q = torch.randn((8, 4, 128), generator=torch.Generator().manual_seed(3)).cuda().bfloat16()
+    want = attention_ref(q, packed, scales, zeros, table, [70, 45], [4, 4], group)
+    for kv in (0, 1):
+        dirty = scales.clone()
+        dirty[table[0, 68 // 16].long(), kv, :, 68 % 16] = bad  # seen by the last two queries of sequence 0
+        out, lse = q4.int4_cache_attention(q, packed, dirty, table, lens, group, zeros=zeros, return_lse=True, path=path)
+        assert not torch.isfinite(out[2:4]).any()
+        assert torch.isfinite(lse[2:4]).all() if kv else torch.isnan(lse[2:4]).all()
+        keep = [0, 1, 4, 5, 6, 7]
+        assert_attention_close((out[keep], lse[keep]), tuple(x[keep] for x in want))
+
+
+@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE])
 def test_attention_unknown_pages_hold_no_tokens(path):
     q, packed, scales, zeros, table, lens, group = attention_setup(lens=(200, 33, 64))
     table[0, 2], table[0, 5], table[2, :] = -7, packed.shape[0], 1 << 30
