@@ -60,7 +60,7 @@ struct AttentionArgs {
   int64_t table_stride;
   const int32_t* kv_lens;   // [batch]
   const int32_t* q_starts;  // [batch + 1], or nullptr: rows / batch queries each
-  int64_t rows;
+  int32_t rows;  // rows * q_heads is below 2^31: so are all row indexes
   int32_t batch;
   int32_t max_pages;
   int32_t q_heads;
@@ -70,36 +70,30 @@ struct AttentionArgs {
   float sm_scale;
 
   // Cached tokens of sequence b, never more than its row of the table holds.
-  __device__ __forceinline__ int64_t kv_len(int b) const {
+  __device__ __forceinline__ int kv_len(int b) const {
     const int64_t cap = static_cast<int64_t>(max_pages) * cache.page_size;
-    const int64_t n = __ldg(kv_lens + b);
-    return n < 0 ? 0 : (n < cap ? n : cap);
+    const int n = max(__ldg(kv_lens + b), 0);
+    return n < cap ? n : static_cast<int>(cap);
   }
   // First query row of sequence b and their number, inside [0, rows).
-  __device__ __forceinline__ void queries(int b, int64_t& first, int64_t& count) const {
+  __device__ __forceinline__ void queries(int b, int& first, int& count) const {
     if (q_starts == nullptr) {
       count = rows / batch;
       first = count * b;
       return;
     }
-    int64_t a = __ldg(q_starts + b), z = __ldg(q_starts + b + 1);
-    a = a < 0 ? 0 : (a < rows ? a : rows);
-    z = z < a ? a : (z < rows ? z : rows);
-    first = a;
-    count = z - a;
+    first = min(max(__ldg(q_starts + b), 0), rows);
+    count = max(min(__ldg(q_starts + b + 1), rows) - first, 0);
   }
-  // Keys that the query at position `pos` of a sequence of `len` tokens sees.
-  __device__ __forceinline__ void visible(int64_t pos, int64_t len, int64_t& lo, int64_t& hi) const {
-    hi = causal != 0 && pos + 1 < len ? pos + 1 : len;
-    lo = window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0;
-    if (hi < 0) hi = 0;
+  // Keys [lo, hi) that the query at position `pos` of a sequence of `len`
+  // tokens sees (none where hi <= lo).
+  __device__ __forceinline__ void visible(int pos, int len, int& lo, int& hi) const {
+    hi = causal != 0 ? max(min(pos + 1, len), 0) : len;
+    lo = window > 0 ? max(pos - window + 1, 0) : 0;
   }
   // The sequence that holds query row t, or -1.
-  __device__ __forceinline__ int sequence_of(int64_t t) const {
-    if (q_starts == nullptr) {
-      const int64_t b = t / (rows / batch);
-      return b < batch ? static_cast<int>(b) : -1;
-    }
+  __device__ __forceinline__ int sequence_of(int t) const {
+    if (q_starts == nullptr) return t / (rows / batch);
     int lo = 0, hi = batch;  // last b with q_starts[b] <= t
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;

@@ -28,16 +28,16 @@ template <typename T, bool ASYM, int BYTES>  // BYTES: bytes of a row per lane
 __global__ void __launch_bounds__(32 * kWarps) attention_any_kernel(
     const __grid_constant__ AttentionArgs a) {
   const CacheView& c = a.cache;
-  const int64_t t = blockIdx.x / a.q_heads;
-  const int hq = static_cast<int>(blockIdx.x - t * a.q_heads);
+  const int t = blockIdx.x / a.q_heads;
+  const int hq = blockIdx.x - t * a.q_heads;
   const int b = a.sequence_of(t);
   if (b < 0) return;  // a row of no sequence stays as it is
   const int h = hq / a.ratio;
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
-  int64_t first, count, lo, hi;
+  int first, count, lo, hi;
   a.queries(b, first, count);
-  const int64_t len = a.kv_len(b);
+  const int len = a.kv_len(b);
   a.visible(len - count + (t - first), len, lo, hi);
 
   float q[2 * BYTES], o[2 * BYTES];
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_any_kernel(
   }
   float m = __int_as_float(0xFF800000), l = 0.0f;  // in units of log2
   const float to_log2 = a.sm_scale * kLog2e;
-  for (int64_t j = lo + warp; j < hi; j += kWarps) {
+  for (int j = lo + warp; j < hi; j += kWarps) {
     const int64_t page = __ldg(a.page_table + b * a.table_stride + j / c.page_size);
     if (page < 0 || page >= c.pages) continue;  // no such page: its tokens are not there
     const int64_t kr = c.row(page, 0, h, j % c.page_size);
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_any_kernel(
   const float base = top == __int_as_float(0xFF800000) ? 0.0f : top;
   float total = 0.0f;
   for (int w = 0; w < kWarps; ++w) total = fmaf(sl[w], exp2f(sm[w] - base), total);
-  const int64_t at = t * a.q_heads + hq;
+  const int64_t at = static_cast<int64_t>(t) * a.q_heads + hq;
   for (int d = threadIdx.x; d < c.head_dim; d += blockDim.x) {
     float v = 0.0f;
     for (int w = 0; w < kWarps; ++w) v = fmaf(so[w][d], exp2f(sm[w] - base), v);
@@ -127,9 +127,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_any_kernel(
 
 template <typename T, bool ASYM>
 cudaError_t launch_any_typed(const AttentionArgs& a, cudaStream_t stream) {
-  const int64_t grid = a.rows * a.q_heads;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const unsigned n = static_cast<unsigned>(grid);
+  const unsigned n = static_cast<unsigned>(a.rows) * a.q_heads;
   const int bytes = (a.cache.row_bytes + 31) / 32;
   if (bytes <= 2)
     attention_any_kernel<T, ASYM, 2><<<n, 32 * kWarps, 0, stream>>>(a);
@@ -163,12 +161,16 @@ cudaError_t launch_cache_attention_any(const AttentionArgs& a, DType t, cudaStre
 // elements in groups of 32, 64, 128 or the whole head, and pages of a power
 // of two of tokens, at least 16 (a block of 16 tokens then lies in one page).
 // Token positions are 32-bit there, with room for a look-ahead of 16 steps.
-bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out, int64_t max_pages) {
+// All counts of steps are 32-bit too.
+bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out, int64_t rows, int64_t batch,
+                                   int ratio, int64_t max_pages) {
   const int d = c.head_dim, g = c.group;
   const bool shape = (d == 64 || d == 96 || d == 128 || d == 256) && d % g == 0 &&
                      (g == 32 || g == d || (d != 96 && (g == 64 || g == 128)));
   const bool pages = c.page_size >= 16 && (c.page_size & (c.page_size - 1)) == 0 &&
-                     max_pages * c.page_size <= (1LL << 30);
+                     max_pages * c.page_size <= (1LL << 30) &&
+                     static_cast<double>(c.heads) * (static_cast<double>(rows) * ratio / 8 + batch) *
+                             (static_cast<double>(max_pages) * c.page_size / kAttnStep + 1) < 0x40000000;
   return t != DType::F32 && shape && pages && multiple_of(c.packed, 16) && multiple_of(c.scales, 16) &&
          multiple_of(c.zeros, 16) && multiple_of(out, 8);
 }

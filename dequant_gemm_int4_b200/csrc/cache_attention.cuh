@@ -55,10 +55,10 @@ constexpr int kAttnStep = kAttnWarps * kAttnTokens;    // tokens of a block's st
 
 // Where the pieces of split items go, in the caller's workspace.
 inline size_t attention_prefix_bytes(int64_t batch) {
-  return (static_cast<size_t>(batch + 1) * 8 + 255) / 256 * 256;
+  return (static_cast<size_t>(batch + 1) * 4 + 255) / 256 * 256;
 }
 struct AttentionSpace {
-  int64_t* prefix;  // [batch + 1]: units of the sequences before each
+  int32_t* prefix;  // [batch + 1]: units of the sequences before each
   float* o;         // [2 * blocks][RT][D]: sums relative to the piece's maximum
   float* ml;        // [2 * blocks][RT][2]: maximum (log2) and sum
   int blocks;
@@ -69,30 +69,29 @@ struct AttentionSpace {
 // steps.
 struct RowTile {
   int lo, hi, steps;
-  __device__ __forceinline__ void set(const AttentionArgs& a, int64_t len, int64_t count, int rt, int RT) {
-    const int64_t r0 = static_cast<int64_t>(rt) * RT;
-    const int64_t rows = count * a.ratio;
-    const int64_t r1 = (r0 + RT < rows ? r0 + RT : rows) - 1;
-    int64_t lo0, hi0, lo1, hi1;
+  __device__ __forceinline__ void set(const AttentionArgs& a, int len, int count, int rt, int RT) {
+    const int r0 = rt * RT;
+    const int r1 = min(r0 + RT, count * a.ratio) - 1;
+    int lo0, hi0, lo1, hi1;
     a.visible(len - count + r0 / a.ratio, len, lo0, hi0);
     a.visible(len - count + r1 / a.ratio, len, lo1, hi1);
-    lo = static_cast<int>(lo0) & ~(kAttnTokens - 1);
-    hi = static_cast<int>(hi1);
+    lo = lo0 & ~(kAttnTokens - 1);
+    hi = hi1;
     steps = hi > lo ? (hi - lo + kAttnStep - 1) / kAttnStep : 0;
   }
 };
 
-__device__ __forceinline__ int row_tiles(const AttentionArgs& a, int64_t count, int RT) {
-  return static_cast<int>((count * a.ratio + RT - 1) / RT);
+__device__ __forceinline__ int row_tiles(const AttentionArgs& a, int count, int RT) {
+  return (count * a.ratio + RT - 1) / RT;
 }
 
 // Steps of one head of sequence b, over all its row tiles.
-__device__ __forceinline__ int64_t head_units(const AttentionArgs& a, int b, int RT) {
-  int64_t first, count;
+__device__ __forceinline__ int head_units(const AttentionArgs& a, int b, int RT) {
+  int first, count;
   a.queries(b, first, count);
-  const int64_t len = a.kv_len(b);
+  const int len = a.kv_len(b);
   const int n = row_tiles(a, count, RT);
-  int64_t u = 0;
+  int u = 0;
   for (int rt = 0; rt < n; ++rt) {
     RowTile r;
     r.set(a, len, count, rt, RT);
@@ -101,18 +100,21 @@ __device__ __forceinline__ int64_t head_units(const AttentionArgs& a, int b, int
   return u;
 }
 
-// Blocks that take part, and the first unit of block c, when there are
-// `units` in all.
-__device__ __forceinline__ int64_t active_blocks(int64_t units, int blocks) {
-  return units < blocks ? units : blocks;
-}
-__device__ __forceinline__ int64_t share_begin(int64_t units, int64_t active, int64_t c) {
-  return c * units / active;
-}
-// The block whose share holds unit u: the largest c with c units / active <= u.
-__device__ __forceinline__ int64_t share_of(int64_t units, int64_t active, int64_t u) {
-  return ((u + 1) * active - 1) / units;
-}
+// How `units` steps are shared: the first `more` blocks take `each` + 1, the
+// other active ones `each`.
+struct Shares {
+  int units, active, each, more;
+  __device__ __forceinline__ Shares(int units_, int blocks) : units(units_), active(min(units_, blocks)) {
+    each = active > 0 ? units / active : 0;
+    more = units - each * active;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c * each + min(c, more); }
+  // The block whose share holds unit u.
+  __device__ __forceinline__ int block_of(int u) const {
+    const int in_larger = more * (each + 1);
+    return u < in_larger ? u / (each + 1) : more + (u - in_larger) / each;
+  }
+};
 
 template <int D_, int GROUP_, int NT_, bool ASYM_>
 struct AttnCfg {
@@ -241,24 +243,23 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
   int* const s_hi = s_lo + RT;                                  // [RT]
   float* const s_m = reinterpret_cast<float*>(s_hi + RT);       // [warps][RT]
   float* const s_l = s_m + kAttnWarps * RT;                     // [warps][RT]
-  __shared__ int64_t s_scan[kAttnWarps];
-  __shared__ int64_t s_off;
-  __shared__ int s_b;
+  __shared__ int s_scan[kAttnWarps];
+  __shared__ int s_off, s_b;
 
   // ---- This block's share: units [u0, u1) of all, beginning in sequence b.
-  int64_t units = 0, mine = 0, upto = 0;
+  int units = 0, mine = 0, upto = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kAttnThreads) {
     const int b = b0 + tid;
     mine = b < a.batch ? head_units(a, b, RT) * cache.heads : 0;
     upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += v;
     }
     if (lane == 31) s_scan[warp] = upto;
     __syncthreads();
-    int64_t all = 0;
+    int all = 0;
     for (int w = 0; w < kAttnWarps; ++w) {
       if (w < warp) upto += s_scan[w];
       all += s_scan[w];
@@ -269,29 +270,29 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
     __syncthreads();
   }
   if (blockIdx.x == 0 && tid == 0) ws.prefix[0] = 0;
-  const int64_t active = active_blocks(units, ws.blocks);
-  if (static_cast<int64_t>(blockIdx.x) >= active) return;
-  const int64_t u0 = share_begin(units, active, blockIdx.x);
-  int64_t left = share_begin(units, active, blockIdx.x + 1) - u0;
+  const Shares shares(units, ws.blocks);
+  if (static_cast<int>(blockIdx.x) >= shares.active) return;
+  const int u0 = shares.begin(blockIdx.x);
+  int left = shares.begin(blockIdx.x + 1) - u0;
   if (a.batch <= kAttnThreads) {
     if (upto - mine <= u0 && u0 < upto) {
       s_b = tid;
       s_off = u0 - (upto - mine);
     }
   } else {
-    int64_t before = 0;
+    int before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kAttnThreads) {
       const int b = b0 + tid;
       mine = b < a.batch ? head_units(a, b, RT) * cache.heads : 0;
       upto = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += v;
       }
       if (lane == 31) s_scan[warp] = upto;
       __syncthreads();
-      int64_t all = 0;
+      int all = 0;
       for (int w = 0; w < kAttnWarps; ++w) {
         if (w < warp) upto += s_scan[w];
         all += s_scan[w];
@@ -310,38 +311,38 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
 
   // ---- The item in which the share begins.
   int b = s_b;
-  int64_t first, count;
+  int first, count;
   a.queries(b, first, count);
-  int64_t len = a.kv_len(b);
+  int len = a.kv_len(b);
   int n_rt = row_tiles(a, count, RT);
   int h, rt = 0, s0;
   RowTile tile;
   {
-    const int64_t per_head = head_units(a, b, RT);
-    int64_t off = s_off;
-    h = static_cast<int>(off / per_head);
+    const int per_head = head_units(a, b, RT);
+    int off = s_off;
+    h = off / per_head;
     off -= h * per_head;
     tile.set(a, len, count, 0, RT);
     while (off >= tile.steps) {
       off -= tile.steps;
       tile.set(a, len, count, ++rt, RT);
     }
-    s0 = static_cast<int>(off);
+    s0 = off;
   }
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * C::kStages * C::kStage;
 
   while (left > 0) {
-    const int n = left < tile.steps - s0 ? static_cast<int>(left) : tile.steps - s0;
-    const int64_t r0 = static_cast<int64_t>(rt) * RT;
-    const int rows = count * a.ratio - r0 < RT ? static_cast<int>(count * a.ratio - r0) : RT;
+    const int n = min(left, tile.steps - s0);
+    const int r0 = rt * RT;
+    const int rows = min(count * a.ratio - r0, RT);
 
     // ---- Queries of the tile: fp16 in fragment order, group sums, bounds.
     for (int r = warp; r < RT; r += kAttnWarps) {
       float v[DB];
       const bool live = r < rows;
-      const int64_t i = live ? (r0 + r) / a.ratio : 0;
-      const int hq = h * a.ratio + (live ? static_cast<int>((r0 + r) - i * a.ratio) : 0);
+      const int i = live ? (r0 + r) / a.ratio : 0;
+      const int hq = h * a.ratio + (live ? r0 + r - i * a.ratio : 0);
       const T* qp = static_cast<const T*>(a.q) + (first + i) * a.q_token_stride + hq * a.q_head_stride;
       float top = 0.0f;
 #pragma unroll
@@ -373,10 +374,10 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
         }
       }
       if (lane == 0) {
-        int64_t lo = 0, hi = 0;
+        int lo = 0, hi = 0;
         if (live) a.visible(len - count + i, len, lo, hi);
-        s_lo[r] = static_cast<int>(lo);
-        s_hi[r] = static_cast<int>(hi);
+        s_lo[r] = lo;
+        s_hi[r] = hi;
         s_f[r] = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23) * (a.sm_scale * 1.4426950408889634f);
       }
     }
@@ -415,6 +416,9 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
 
     // ---- Copies: page ids 16 tiles at a time, a lane per block of 16 tokens.
     const int tile_base = tile.lo + s0 * kAttnStep + warp * kAttnTokens;
+    const int64_t page_rows = static_cast<int64_t>(2 * cache.heads) << page_shift;
+    const int64_t head_row = static_cast<int64_t>(h) << page_shift;
+    const int64_t to_values = static_cast<int64_t>(cache.heads) << page_shift;
     int page_ids = -1;
     uint32_t live_blocks = 0u;  // two bits a stage
     auto issue = [&](int k, int stage) {
@@ -431,22 +435,28 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
         const int id0 = __shfl_sync(0xffffffffu, page_ids, (k & 15) * 2);
         const int id1 = __shfl_sync(0xffffffffu, page_ids, (k & 15) * 2 + 1);
         const int mask = cache.page_size - 1;
-        // Rows of the two blocks' first tokens, keys; values lie `vrows` on.
-        const int64_t row0 = cache.row(id0, 0, h, tok0 & mask);
-        const int64_t row1 = cache.row(id1, 0, h, (tok0 + 16) & mask);
-        const int64_t vrows = static_cast<int64_t>(cache.heads) << page_shift;
+        // The blocks' first rows within their head's keys, then their first
+        // bytes.  A block's 16 rows are contiguous; values lie `to_values` on.
+        const int64_t row0 = static_cast<int64_t>(id0) * page_rows + head_row + (tok0 & mask);
+        const int64_t row1 = static_cast<int64_t>(id1) * page_rows + head_row + ((tok0 + 16) & mask);
         const uint32_t dst = ring + stage * C::kStage;
+        const uint8_t* const code0 = cache.packed + row0 * RB + lane * 16;
+        const uint8_t* const code1 = cache.packed + row1 * RB + lane * 16;
+        constexpr int kHalf = RC * 16;  // chunks of a block
 #pragma unroll
-        for (int i = 0; i < RC; ++i) {
-          const int q = i * 32 + lane;
-          const int r = q / RC, c = q % RC;
-          const bool second = r >= 16;
-          if ((second ? id1 : id0) >= 0) {
-            const uint8_t* src =
-                cache.packed + ((second ? row1 - 16 : row0) + r) * RB + c * 16;
+        for (int i = 0; i < kHalf; i += 32) {
+          if (kHalf % 32 == 0 || i + lane < kHalf) {
+            // Chunk i + lane of a block: its row and place follow from the lane.
+            const int r = (i + lane) / RC, c = (i + lane) % RC;
             const uint32_t at = dst + r * RB + chunk_of<RB>(r, c) * 16;
-            cp16(at, src);
-            cp16(at + C::kCodes, src + vrows * RB);
+            if (id0 >= 0) {
+              cp16(at, code0 + i * 16);
+              cp16(at + C::kCodes, code0 + i * 16 + to_values * RB);
+            }
+            if (id1 >= 0) {
+              cp16(at + 16 * RB, code1 + i * 16);
+              cp16(at + 16 * RB + C::kCodes, code1 + i * 16 + to_values * RB);
+            }
           }
         }
         // Scales: a block's 16 NG halves are 2 NG chunks, keys then values.
@@ -456,7 +466,7 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
           const int kv = i / (4 * NG), blk = (i / (2 * NG)) & 1, c = i % (2 * NG);
           if (i < 8 * NG && (blk ? id1 : id0) >= 0)
             cp16(dst + C::kScaleAt + kv * C::kScales + blk * 32 * NG + c * 16,
-                 cache.scales + ((blk ? row1 : row0) + kv * vrows) * NG + c * 8);
+                 cache.scales + ((blk ? row1 : row0) + kv * to_values) * NG + c * 8);
         }
         if (ASYM) {
 #pragma unroll
@@ -465,7 +475,7 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
             const int kv = i / (2 * NG), blk = (i / NG) & 1, c = i % NG;
             if (i < 4 * NG && (blk ? id1 : id0) >= 0)
               cp16(dst + C::kZeroAt + kv * C::kZeros + blk * 16 * NG + c * 16,
-                   cache.zeros + ((blk ? row1 : row0) + kv * vrows) * NG + c * 16);
+                   cache.zeros + ((blk ? row1 : row0) + kv * to_values) * NG + c * 16);
           }
         }
         const uint32_t live = (id0 >= 0 ? 1u : 0u) | (id1 >= 0 ? 2u : 0u);
@@ -753,8 +763,8 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
         }
       }
       __syncthreads();
-      for (int i = tid; i < 8 * (D / 4); i += kAttnThreads) {
-        const int rr = i / (D / 4), d = (i % (D / 4)) * 4;
+      for (int k = tid; k < 8 * (D / 4); k += kAttnThreads) {
+        const int rr = k / (D / 4), d = (k % (D / 4)) * 4;
         const int r = nt * 8 + rr;
         if (r >= rows) continue;
         float4 v = *reinterpret_cast<const float4*>(buf + rr * C::kMergePitch + d);
@@ -772,10 +782,10 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
           sum += s_l[w * RT + r] * (mw == top ? 1.0f : ex2(mw - top));
         }
         if (whole) {
-          const int64_t i_tok = (r0 + r) / a.ratio;
-          const int64_t at = (first + i_tok) * a.q_heads + h * a.ratio + ((r0 + r) - i_tok * a.ratio);
+          const int i = (r0 + r) / a.ratio;
+          const int at = (first + i) * a.q_heads + h * a.ratio + (r0 + r - i * a.ratio);
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          T* out = static_cast<T*>(a.out) + at * D + d;
+          T* out = static_cast<T*>(a.out) + static_cast<int64_t>(at) * D + d;
           alignas(8) T four[4];
           store_as(four, v.x * inv);
           store_as(four + 1, v.y * inv);
@@ -829,18 +839,18 @@ __global__ void __launch_bounds__(256)
   __shared__ float part[8][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int D = a.cache.head_dim;
-  const int64_t index = static_cast<int64_t>(blockIdx.x) * (8 / wpr) + warp / wpr;
-  const int64_t tok = index / a.q_heads;
-  const int hq = static_cast<int>(index - tok * a.q_heads);
+  const int index = blockIdx.x * (8 / wpr) + warp / wpr;
+  const int tok = index / a.q_heads;
+  const int hq = index - tok * a.q_heads;
   int b = -1;
   if (tok < a.rows) b = a.sequence_of(tok);
-  int64_t first = 0, count = 0, r = 0, before = 0, per_head = 0, p_end = 0, p0 = 0;
-  int steps = 0, rt = 0;
+  int r = 0, before = 0, per_head = 0, p_end = 0, p0 = 0, steps = 0, rt = 0;
   if (b >= 0) {
+    int first, count;
     a.queries(b, first, count);
-    const int64_t len = a.kv_len(b);
+    const int len = a.kv_len(b);
     r = (tok - first) * a.ratio + hq % a.ratio;
-    rt = static_cast<int>(r / RT);
+    rt = r / RT;
     const int n = row_tiles(a, count, RT);
     for (int i = 0; i < n; ++i) {
       RowTile tile;
@@ -851,33 +861,31 @@ __global__ void __launch_bounds__(256)
     }
   }
   ptx::grid_dependency_wait();
-  int64_t active = 1;
   if (steps > 0) {
-    const int64_t units = ws.prefix[a.batch];
-    active = active_blocks(units, ws.blocks);
-    const int64_t begin = ws.prefix[b] + (hq / a.ratio) * per_head + before;
-    p0 = share_of(units, active, begin);
-    p_end = share_of(units, active, begin + steps - 1) + 1;
+    const Shares shares(ws.prefix[a.batch], ws.blocks);
+    const int begin = ws.prefix[b] + (hq / a.ratio) * per_head + before;
+    p0 = shares.block_of(begin);
+    p_end = shares.block_of(begin + steps - 1) + 1;
   }
   const bool join = p_end - p0 > 1;
   const bool empty = b >= 0 && steps == 0;
   float4 v[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   float top = kNegInf, sum = 0.0f;
-  const int rr = static_cast<int>(r - static_cast<int64_t>(rt) * RT);
+  const int rr = r - rt * RT;
   if (join) {
     // The first piece ends its block's share, every other one begins its own.
-    auto slot = [&](int64_t p) { return (2 * p + (p == p0 ? 1 : 0)) * RT + rr; };
-    for (int64_t p = p0 + lane; p < p_end; p += 32) top = fmaxf(top, ws.ml[slot(p) * 2]);
+    auto slot = [&](int p) { return (2 * p + (p == p0 ? 1 : 0)) * RT + rr; };
+    for (int p = p0 + lane; p < p_end; p += 32) top = fmaxf(top, ws.ml[slot(p) * 2]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int64_t p = p0 + lane; p < p_end; p += 32) {
+    for (int p = p0 + lane; p < p_end; p += 32) {
       const float mp = ws.ml[slot(p) * 2];
       sum += ws.ml[slot(p) * 2 + 1] * (mp == top ? 1.0f : attn::ex2(mp - top));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
 #pragma unroll 4
-    for (int64_t p = p0 + warp % wpr; p < p_end; p += wpr) {
+    for (int p = p0 + warp % wpr; p < p_end; p += wpr) {
       const int64_t s = slot(p);
       const float mp = ws.ml[s * 2];
       const float w = mp == top ? 1.0f : attn::ex2(mp - top);
@@ -912,7 +920,7 @@ __global__ void __launch_bounds__(256)
     }
   }
   if (!join && !empty) return;
-  const int64_t at = tok * a.q_heads + hq;
+  const int64_t at = index;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -951,7 +959,7 @@ cudaError_t launch_attention_cfg(const AttentionArgs& a, void* workspace, cudaSt
   AttentionSpace ws;
   ws.blocks = attention_blocks<C>();
   uint8_t* p = static_cast<uint8_t*>(workspace);
-  ws.prefix = reinterpret_cast<int64_t*>(p);
+  ws.prefix = reinterpret_cast<int32_t*>(p);
   p += attention_prefix_bytes(a.batch);
   ws.o = reinterpret_cast<float*>(p);
   ws.ml = ws.o + 2LL * ws.blocks * C::RT * C::D;
@@ -964,7 +972,7 @@ cudaError_t launch_attention_cfg(const AttentionArgs& a, void* workspace, cudaSt
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // The join starts while the last shares are finished.
-  const int64_t rows = a.rows * a.q_heads;
+  const int rows = a.rows * a.q_heads;
   const int wpr = rows <= 2048 ? 8 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(wpr == 8 ? rows : (rows + 7) / 8));

@@ -452,7 +452,7 @@ static int attention_plan(const char* name, const int4lib::CacheView& view, DTyp
                   name);
     return int4lib::fail(INT4_ERR_ARG, msg);
   }
-  *mma = int4lib::cache_attention_mma_supported(view, t, out, max_pages);
+  *mma = int4lib::cache_attention_mma_supported(view, t, out, rows, batch, q_heads / view.heads, max_pages);
   if (path == INT4_PATH_DECODE && !*mma) {
     std::snprintf(msg, sizeof msg, "%s: the tensor-core kernels cannot run this call", name);
     return int4lib::fail(INT4_ERR_UNSUPPORTED, msg);
@@ -520,7 +520,7 @@ int int4_cache_attention(const int4_cache* cache, const void* q, int64_t q_token
     return int4lib::fail(INT4_ERR_ARG, msg);
   }
   const int4lib::AttentionArgs a = {view, q, q_token_stride, q_head_stride, out, lse, page_table,
-                                    table_stride, kv_lens, q_starts, rows, batch, max_pages, q_heads,
+                                    table_stride, kv_lens, q_starts, static_cast<int32_t>(rows), batch, max_pages, q_heads,
                                     q_heads / view.heads, causal != 0 ? 1 : 0, window, sm_scale};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = mma ? int4lib::launch_cache_attention_mma(a, t, workspace, s)

@@ -96,7 +96,8 @@ cudaError_t launch_cache_read(const CacheView& cache, const int64_t* slots, int6
 // cache_attention.cu: any shape, and the tensor-core kernels with their
 // workspace (any content).
 cudaError_t launch_cache_attention_any(const AttentionArgs& a, DType t, cudaStream_t stream);
-bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out, int64_t max_pages);
+bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out, int64_t rows, int64_t batch,
+                                   int ratio, int64_t max_pages);
 size_t cache_attention_mma_workspace(const CacheView& c, int64_t rows, int64_t batch, int ratio);
 cudaError_t launch_cache_attention_mma(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
 // cache_attention_<D>.cu: the kernels for heads of D elements; rt: query rows
