@@ -170,7 +170,7 @@ bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out,
   const bool pages = c.page_size >= 16 && (c.page_size & (c.page_size - 1)) == 0 &&
                      max_pages * c.page_size <= (1LL << 30) &&
                      static_cast<double>(c.heads) * (static_cast<double>(rows) * ratio / 8 + batch) *
-                             (static_cast<double>(max_pages) * c.page_size / kAttnStep + 1) < 0x40000000;
+                             (static_cast<double>(max_pages) * c.page_size / 128 + 1) < 0x40000000;
   return t != DType::F32 && shape && pages && multiple_of(c.packed, 16) && multiple_of(c.scales, 16) &&
          multiple_of(c.zeros, 16) && multiple_of(out, 8);
 }

@@ -42,6 +42,8 @@
 // replayed with other lengths.
 #pragma once
 
+#include <type_traits>
+
 #include "cache.cuh"
 #include "internal.h"
 #include "sm100_ptx.cuh"
@@ -50,8 +52,10 @@ namespace int4lib {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kAttnTokens = 32;                        // tokens of a warp's tile
-constexpr int kAttnStep = kAttnWarps * kAttnTokens;    // tokens of a block's step
+// Tokens of a warp's tile and of a block's step, by the row tile: 64 while the
+// scores of 8 rows fit beside the accumulators, else 32.
+__host__ __device__ constexpr int attention_tokens(int head_dim, int rt) { return rt == 8 && head_dim <= 128 ? 64 : 32; }
+__host__ __device__ constexpr int attention_step(int head_dim, int rt) { return kAttnWarps * attention_tokens(head_dim, rt); }
 
 // Where the pieces of split items go, in the caller's workspace.
 inline size_t attention_prefix_bytes(int64_t batch) {
@@ -65,19 +69,20 @@ struct AttentionSpace {
 };
 
 // Row tile `rt` (rows [rt RT, (rt + 1) RT) of a sequence's query tokens x
-// ratio): the tokens it needs, from lo (a multiple of 32) to hi, and its
-// steps.
+// ratio): the tokens it needs, from lo (a multiple of a warp's tile) to hi,
+// and its steps.
 struct RowTile {
   int lo, hi, steps;
   __device__ __forceinline__ void set(const AttentionArgs& a, int len, int count, int rt, int RT) {
+    const int step = attention_step(a.cache.head_dim, RT);
     const int r0 = rt * RT;
     const int r1 = min(r0 + RT, count * a.ratio) - 1;
     int lo0, hi0, lo1, hi1;
     a.visible(len - count + r0 / a.ratio, len, lo0, hi0);
     a.visible(len - count + r1 / a.ratio, len, lo1, hi1);
-    lo = lo0 & ~(kAttnTokens - 1);
+    lo = lo0 & -(step / kAttnWarps);
     hi = hi1;
-    steps = hi > lo ? (hi - lo + kAttnStep - 1) / kAttnStep : 0;
+    steps = hi > lo ? (hi - lo + step - 1) / step : 0;
   }
 };
 
@@ -127,11 +132,13 @@ struct AttnCfg {
   static constexpr int RB = D / 2;             // bytes of a row
   static constexpr int RC = RB / 16;           // 16-byte chunks of a row
   // Blocks on an SM, by the registers of the accumulators (D / 4 NT a lane).
-  static constexpr int kBlocks = D * NT <= 128 ? 4 : (D * NT <= 256 ? 3 : 2);
+  static constexpr int kBlocks = D * NT <= 64 ? 4 : (D * NT <= 256 ? 3 : 2);
   // One warp's tile: keys, values, their scales, their zero points.
-  static constexpr int kCodes = kAttnTokens * RB;
-  static constexpr int kScales = kAttnTokens * NG * 2;
-  static constexpr int kZeros = ASYM ? kAttnTokens * NG : 0;
+  static constexpr int TOK = attention_tokens(D, RT);
+  static constexpr int MB = TOK / 16;          // blocks of 16 tokens
+  static constexpr int kCodes = TOK * RB;
+  static constexpr int kScales = TOK * NG * 2;
+  static constexpr int kZeros = ASYM ? TOK * NG : 0;
   static constexpr int kScaleAt = 2 * kCodes;
   static constexpr int kZeroAt = kScaleAt + 2 * kScales;
   static constexpr int kStage = (kZeroAt + 2 * kZeros + 127) / 128 * 128;
@@ -163,11 +170,11 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
@@ -182,6 +189,25 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with the sum begun at {c0, c1} in both halves of the rows.
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1, float c0, float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Halves of r are zeroed where those of p are zero.
+__device__ __forceinline__ uint32_t zero_where_zero(uint32_t r, uint32_t p) {
+  if ((p & 0x7FFFu) == 0u) r &= 0xFFFF0000u;
+  if ((p & 0x7FFF0000u) == 0u) r &= 0x0000FFFFu;
+  return r;
 }
 // (w ^ flip) & mask in one operation.
 template <bool ASYM>
@@ -228,7 +254,8 @@ template <typename T, class C>
 __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
     attention_mma_kernel(const __grid_constant__ AttentionArgs a, const AttentionSpace ws, const int page_shift) {
   using namespace attn;
-  constexpr int D = C::D, NT = C::NT, RT = C::RT, DB = C::DB, NG = C::NG, RB = C::RB, RC = C::RC;
+  constexpr int D = C::D, NT = C::NT, RT = C::RT, DB = C::DB, NG = C::NG, RB = C::RB, RC = C::RC, MB = C::MB, TOK = C::TOK;
+  constexpr int kStep = kAttnWarps * TOK;
   constexpr bool ASYM = C::ASYM;
   constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -330,12 +357,94 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
     s0 = off;
   }
 
+  // q takes the sign of sm_scale.
+  const float sign = a.sm_scale > 0.0f ? 1.0f : (a.sm_scale < 0.0f ? -1.0f : 0.0f);
+  const int split = max(0, (TOK == 64 ? 6 : 5) - page_shift);
   const uint32_t ring = ptx::smem_u32(smem) + warp * C::kStages * C::kStage;
 
   while (left > 0) {
     const int n = min(left, tile.steps - s0);
     const int r0 = rt * RT;
     const int rows = min(count * a.ratio - r0, RT);
+
+    // ---- Copies.  A lane keeps the page of a tile, or where pages are smaller
+    // than tiles of one of its 2^split parts.
+    const int tile_base = tile.lo + s0 * kStep + warp * TOK;
+    const int64_t page_rows = static_cast<int64_t>(2 * cache.heads) << page_shift;
+    const int64_t head_row = static_cast<int64_t>(h) << page_shift;
+    const int64_t to_values = static_cast<int64_t>(cache.heads) << page_shift;
+    int page_ids = -1;
+    uint32_t live_blocks = 0u;  // MB bits a stage: which blocks of 16 tokens are there
+    auto issue = [&](int k, int stage) {
+      if (k < n) {
+        const int in_ids = k & ((32 >> split) - 1);
+        if (in_ids == 0) {
+          const int tok = tile_base + (k + (lane >> split)) * kStep + ((lane & ((1 << split) - 1)) << page_shift);
+          page_ids = -1;
+          if (tok < tile.hi) {
+            const int id = __ldg(a.page_table + b * a.table_stride + (tok >> page_shift));
+            page_ids = id >= 0 && id < cache.pages ? id : -1;
+          }
+        }
+        const uint32_t dst = ring + stage * C::kStage;
+        const int tok0 = tile_base + k * kStep;
+        uint32_t live = 0u;
+        // Rows of one page are contiguous, keys and values apart: `blocks`
+        // blocks of 16 tokens from row `row` on, at block `at` of the tile.
+        auto copy = [&](auto blocks, int64_t row, int at) {
+          constexpr int B = decltype(blocks)::value;
+          const uint8_t* const k_src = cache.packed + (head_row + row) * RB + lane * 16;
+          const uint8_t* const v_src = k_src + to_values * RB;
+#pragma unroll
+          for (int i = 0; i < B * 16 * RC; i += 32) {
+            if ((B * 16 * RC) % 32 == 0 || i + lane < B * 16 * RC) {
+              const int r = (i + lane) / RC, c = (i + lane) % RC;
+              const uint32_t to = dst + at * 16 * RB + r * RB + chunk_of<RB>(r, c) * 16;
+              cp16(to, k_src + i * 16);
+              cp16(to + C::kCodes, v_src + i * 16);
+            }
+          }
+          constexpr int kSc = B * 2 * NG, kZe = B * NG;  // chunks of the scales, of the zero points
+#pragma unroll
+          for (int i0 = 0; i0 < 2 * kSc; i0 += 32) {
+            const int i = i0 + lane, kv = i / kSc, c = i % kSc;
+            if (i < 2 * kSc)
+              cp16(dst + C::kScaleAt + kv * C::kScales + at * 32 * NG + c * 16,
+                   cache.scales + (head_row + row + kv * to_values) * NG + c * 8);
+          }
+          if (ASYM) {
+#pragma unroll
+            for (int i0 = 0; i0 < 2 * kZe; i0 += 32) {
+              const int i = i0 + lane, kv = i / kZe, c = i % kZe;
+              if (i < 2 * kZe)
+                cp16(dst + C::kZeroAt + kv * C::kZeros + at * 16 * NG + c * 16,
+                     cache.zeros + (head_row + row + kv * to_values) * NG + c * 16);
+            }
+          }
+        };
+        if (split == 0) {
+          const int id = __shfl_sync(0xffffffffu, page_ids, in_ids);
+          if (id >= 0) {
+            live = (1u << MB) - 1;
+            copy(std::integral_constant<int, MB>{}, id * page_rows + (tok0 & (cache.page_size - 1)), 0);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < MB; ++i) {
+            const int id = __shfl_sync(0xffffffffu, page_ids, (in_ids << split) + ((i * 16) >> page_shift));
+            if (id >= 0) {
+              live |= 1u << i;
+              copy(std::integral_constant<int, 1>{}, id * page_rows + ((tok0 + i * 16) & (cache.page_size - 1)), i);
+            }
+          }
+        }
+        live_blocks = (live_blocks & ~(((1u << MB) - 1) << (MB * stage))) | (live << (MB * stage));
+      }
+      cp_commit();
+    };
+    // The first tiles are on their way while the queries are laid out.
+#pragma unroll 1
+    for (int k = 0; k < C::kStages - 1; ++k) issue(k, k);
 
     // ---- Queries of the tile: fp16 in fragment order, group sums, bounds.
     for (int r = warp; r < RT; r += kAttnWarps) {
@@ -355,7 +464,7 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
       // top in [2^e, 2^(e+1)); elements are scaled by 2^(14 - e).
       int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
       e = e < -100 ? -100 : e;
-      const float scale = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+      const float scale = sign * __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
       const int nt = r >> 3, gr = r & 7, tl = lane >> 3, el = lane & 7;
       float sum = 0.0f;
 #pragma unroll
@@ -378,7 +487,9 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
         if (live) a.visible(len - count + i, len, lo, hi);
         s_lo[r] = lo;
         s_hi[r] = hi;
-        s_f[r] = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23) * (a.sm_scale * 1.4426950408889634f);
+        // Positive, so that it may be applied after the maximum.
+        const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23) * (fabsf(a.sm_scale) * 1.4426950408889634f);
+        s_f[r] = sign == 0.0f ? 1.0f : fminf(fmaxf(f1, 0x1p-126f), 0x1p127f);
       }
     }
     __syncthreads();
@@ -398,7 +509,11 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
       qs1[nt] = *reinterpret_cast<const float2*>(s_qsum + nt * 8 + 2 * t);
     }
 
-    float o[DB][2][NT][4], zo[NG][NT][4], m[NT][2], l[NT][2];
+    float o[DB][2][NT][4], zo[NG][NT][4];
+    // Per row: the maximum of S / f, -maximum * f (0 before the first token),
+    // and this lane's part of the sum.
+    float m[NT][2];
+    float2 nmf[NT], l[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -410,120 +525,39 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
 #pragma unroll
         for (int k = 0; k < 4; ++k) zo[gi][nt][k] = 0.0f;
       m[nt][0] = m[nt][1] = kNegInf;
-      l[nt][0] = l[nt][1] = 0.0f;
+      nmf[nt] = l[nt] = make_float2(0.0f, 0.0f);
     }
-    int e_run = 1;  // exponent field of the largest value scale so far
+    int x_run = 15;  // weights are held 2^x_run fold
 
-    // ---- Copies: page ids 16 tiles at a time, a lane per block of 16 tokens.
-    const int tile_base = tile.lo + s0 * kAttnStep + warp * kAttnTokens;
-    const int64_t page_rows = static_cast<int64_t>(2 * cache.heads) << page_shift;
-    const int64_t head_row = static_cast<int64_t>(h) << page_shift;
-    const int64_t to_values = static_cast<int64_t>(cache.heads) << page_shift;
-    int page_ids = -1;
-    uint32_t live_blocks = 0u;  // two bits a stage
-    auto issue = [&](int k, int stage) {
-      if (k < n) {
-        if ((k & 15) == 0) {
-          const int tok = tile_base + (k + (lane >> 1)) * kAttnStep + (lane & 1) * 16;
-          page_ids = -1;
-          if (tok < tile.hi) {
-            const int id = __ldg(a.page_table + b * a.table_stride + (tok >> page_shift));
-            page_ids = id >= 0 && id < cache.pages ? id : -1;
-          }
-        }
-        const int tok0 = tile_base + k * kAttnStep;
-        const int id0 = __shfl_sync(0xffffffffu, page_ids, (k & 15) * 2);
-        const int id1 = __shfl_sync(0xffffffffu, page_ids, (k & 15) * 2 + 1);
-        const int mask = cache.page_size - 1;
-        // The blocks' first rows within their head's keys, then their first
-        // bytes.  A block's 16 rows are contiguous; values lie `to_values` on.
-        const int64_t row0 = static_cast<int64_t>(id0) * page_rows + head_row + (tok0 & mask);
-        const int64_t row1 = static_cast<int64_t>(id1) * page_rows + head_row + ((tok0 + 16) & mask);
-        const uint32_t dst = ring + stage * C::kStage;
-        const uint8_t* const code0 = cache.packed + row0 * RB + lane * 16;
-        const uint8_t* const code1 = cache.packed + row1 * RB + lane * 16;
-        constexpr int kHalf = RC * 16;  // chunks of a block
-#pragma unroll
-        for (int i = 0; i < kHalf; i += 32) {
-          if (kHalf % 32 == 0 || i + lane < kHalf) {
-            // Chunk i + lane of a block: its row and place follow from the lane.
-            const int r = (i + lane) / RC, c = (i + lane) % RC;
-            const uint32_t at = dst + r * RB + chunk_of<RB>(r, c) * 16;
-            if (id0 >= 0) {
-              cp16(at, code0 + i * 16);
-              cp16(at + C::kCodes, code0 + i * 16 + to_values * RB);
-            }
-            if (id1 >= 0) {
-              cp16(at + 16 * RB, code1 + i * 16);
-              cp16(at + 16 * RB + C::kCodes, code1 + i * 16 + to_values * RB);
-            }
-          }
-        }
-        // Scales: a block's 16 NG halves are 2 NG chunks, keys then values.
-#pragma unroll
-        for (int i0 = 0; i0 < 8 * NG; i0 += 32) {
-          const int i = i0 + lane;
-          const int kv = i / (4 * NG), blk = (i / (2 * NG)) & 1, c = i % (2 * NG);
-          if (i < 8 * NG && (blk ? id1 : id0) >= 0)
-            cp16(dst + C::kScaleAt + kv * C::kScales + blk * 32 * NG + c * 16,
-                 cache.scales + ((blk ? row1 : row0) + kv * to_values) * NG + c * 8);
-        }
-        if (ASYM) {
-#pragma unroll
-          for (int i0 = 0; i0 < 4 * NG; i0 += 32) {
-            const int i = i0 + lane;
-            const int kv = i / (2 * NG), blk = (i / NG) & 1, c = i % NG;
-            if (i < 4 * NG && (blk ? id1 : id0) >= 0)
-              cp16(dst + C::kZeroAt + kv * C::kZeros + blk * 16 * NG + c * 16,
-                   cache.zeros + ((blk ? row1 : row0) + kv * to_values) * NG + c * 16);
-          }
-        }
-        const uint32_t live = (id0 >= 0 ? 1u : 0u) | (id1 >= 0 ? 2u : 0u);
-        live_blocks = (live_blocks & ~(3u << (2 * stage))) | (live << (2 * stage));
-      }
-      cp_commit();
-    };
-
-#pragma unroll
-    for (int k = 0; k < C::kStages - 1; ++k) issue(k, k);
     int stage = 0;
+#pragma unroll 1
     for (int k = 0; k < n; ++k) {
       cp_wait<C::kStages - 2>();
       __syncwarp();
       issue(k + C::kStages - 1, stage == 0 ? C::kStages - 1 : stage - 1);
       const uint32_t st = ring + stage * C::kStage;
-      const uint32_t live = (live_blocks >> (2 * stage)) & 3u;
+      const uint32_t live = (live_blocks >> (MB * stage)) & ((1u << MB) - 1);
       stage = stage == C::kStages - 1 ? 0 : stage + 1;
-      const int base = tile_base + k * kAttnStep;
+      const int base = tile_base + k * kStep;
       if (live == 0u) continue;  // past the end, or no page: the warp has no tokens here
 
-      // ---- S^T = K Q^T for two blocks of 16 tokens.
-      float s[2][NT][4];
+      // ---- S^T / f = K Q^T by blocks of 16 tokens; s[mb][nt][half] holds
+      // token mb * 16 + half * 8 + g and rows nt * 8 + 2 t, + 1.
+      float2 s[MB][NT][2];
       {
-        float acc[2][NT][4];
+        float acc[MB][NT][4];
 #pragma unroll
         for (int c = 0; c < DB; ++c) {
           const int gi = c / C::BPG;
-          if (c % C::BPG == 0) {
+          uint32_t kr[2 * MB];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float2 init = make_float2(0.0f, 0.0f);
-              if (!ASYM)
-                init = NG == 1 ? qs1[nt] : *reinterpret_cast<const float2*>(s_qsum + gi * RT + nt * 8 + 2 * t);
-#pragma unroll
-              for (int mb = 0; mb < 2; ++mb) {
-                acc[mb][nt][0] = acc[mb][nt][2] = init.x;
-                acc[mb][nt][1] = acc[mb][nt][3] = init.y;
-              }
-            }
-          }
-          uint32_t kr[4];
-          ldsm4(st + lane * RB + chunk_of<RB>(lane, c) * 16, kr);
+          for (int i = 0; i < MB; i += 2)
+            ldsm4(st + (i * 16 + lane) * RB + chunk_of<RB>(lane, c) * 16, kr + 2 * i);
 #pragma unroll
           for (int step = 0; step < 2; ++step) {
-            uint32_t lo[4], hi[4];
+            uint32_t lo[2 * MB], hi[2 * MB];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2 * MB; ++i) {
               lo[i] = pick<ASYM>(kr[i], 0x000F000Fu);
               hi[i] = pick<ASYM>(kr[i], 0x00F000F0u);
               kr[i] >>= 8;
@@ -533,98 +567,120 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
               const int at = (c * 2 + step) * NT + nt;
               const uint2 q2 = C::kQInRegs ? qf[C::kQInRegs ? at : 0]
                                            : ptx::lds64(ptx::smem_u32(sq) + (at * 32 + lane) * 8);
-              mma(acc[0][nt], lo[0], lo[1], hi[0], hi[1], q2.x, q2.y);
-              mma(acc[1][nt], lo[2], lo[3], hi[2], hi[3], q2.x, q2.y);
+              if (c % C::BPG == 0 && step == 0) {
+                float2 init = make_float2(0.0f, 0.0f);
+                if (!ASYM) init = NG == 1 ? qs1[nt] : lds_f2(ptx::smem_u32(s_qsum + gi * RT + nt * 8 + 2 * t));
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
+                  mma_from(acc[mb][nt], lo[2 * mb], lo[2 * mb + 1], hi[2 * mb], hi[2 * mb + 1], q2.x, q2.y, init.x, init.y);
+              } else {
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
+                  mma(acc[mb][nt], lo[2 * mb], lo[2 * mb + 1], hi[2 * mb], hi[2 * mb + 1], q2.x, q2.y);
+              }
             }
           }
           if (c % C::BPG == C::BPG - 1) {
+            float2 qz[NT];
+            if (ASYM) {
 #pragma unroll
-            for (int mb = 0; mb < 2; ++mb)
+              for (int nt = 0; nt < NT; ++nt)
+                qz[nt] = NG == 1 ? qs1[nt] : lds_f2(ptx::smem_u32(s_qsum + gi * RT + nt * 8 + 2 * t));
+            }
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
                 const int tok = mb * 16 + half * 8 + g;
                 const float k1 = f16_bits_to_float(lds_u16(st + C::kScaleAt + (tok * NG + gi) * 2));
                 const float ks = fmaf(k1, 0x1p24f, k1 * 0.0f);  // an infinite scale gives NaN, as its values do
-                const float kz =
-                    ASYM ? static_cast<float>(lds_u8(st + C::kZeroAt + tok * NG + gi)) : 0.0f;
+                const float2 ks2 = make_float2(ks, ks);
+                float2 kz2 = make_float2(0.0f, 0.0f);
+                if (ASYM) kz2.x = kz2.y = static_cast<float>(lds_u8(st + C::kZeroAt + tok * NG + gi));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  float2 qz = make_float2(0.0f, 0.0f);
-                  if (ASYM)
-                    qz = NG == 1 ? qs1[nt]
-                                 : *reinterpret_cast<const float2*>(s_qsum + gi * RT + nt * 8 + 2 * t);
-                  float x0 = acc[mb][nt][2 * half], x1 = acc[mb][nt][2 * half + 1];
-                  if (ASYM) {
-                    x0 = fmaf(kz, qz.x, x0);
-                    x1 = fmaf(kz, qz.y, x1);
-                  }
-                  s[mb][nt][2 * half] = gi == 0 ? ks * x0 : fmaf(ks, x0, s[mb][nt][2 * half]);
-                  s[mb][nt][2 * half + 1] = gi == 0 ? ks * x1 : fmaf(ks, x1, s[mb][nt][2 * half + 1]);
+                  float2 x = make_float2(acc[mb][nt][2 * half], acc[mb][nt][2 * half + 1]);
+                  if (ASYM) x = __ffma2_rn(kz2, qz[nt], x);
+                  s[mb][nt][half] = gi == 0 ? __fmul2_rn(ks2, x) : __ffma2_rn(ks2, x, s[mb][nt][half]);
                 }
               }
           }
         }
       }
-      // Value scales of this lane's tokens, as fp16 bits.
-      uint32_t vs[2][2][NG];
+      // ---- Value scales of tokens 2t, 2t + 1 of each group of 8: NG words
+      // hold the two tokens' scales; x_new follows their largest exponent
+      // (the OR of the bits bounds it, by less than twice).
+      uint32_t vs[MB][2][NG];
+      uint32_t vbits = 0u;
 #pragma unroll
-      for (int mb = 0; mb < 2; ++mb)
+      for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t va = st + C::kScaleAt + C::kScales + (mb * 16 + half * 8 + 2 * t) * NG * 2;
+          if constexpr (NG % 4 == 0) {
 #pragma unroll
-          for (int gi = 0; gi < NG; ++gi)
-            vs[mb][half][gi] =
-                lds_u16(st + C::kScaleAt + C::kScales + ((mb * 16 + half * 8 + g) * NG + gi) * 2);
+            for (int i = 0; i < NG / 4; ++i) {
+              const uint4 w = ptx::lds128(va + 16 * i);
+              vs[mb][half][4 * i] = w.x;
+              vs[mb][half][4 * i + 1] = w.y;
+              vs[mb][half][4 * i + 2] = w.z;
+              vs[mb][half][4 * i + 3] = w.w;
+            }
+          } else if constexpr (NG == 2) {
+            const uint2 w = ptx::lds64(va);
+            vs[mb][half][0] = w.x;
+            vs[mb][half][1] = w.y;
+          } else {
 #pragma unroll
-      for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[mb][nt][j] *= (j & 1) ? f[nt].y : f[nt].x;
-      // ---- Mask, where some row does not see every token of the tile; the
-      // largest value scale (of an edge tile's finite ones: what is not seen
-      // must not count, and a row that sees another has no finite output).
-      const bool edge = base < all_lo || base + kAttnTokens > all_hi || live != 3u;
-      uint32_t vtop = 0u;
+            for (int i = 0; i < NG; ++i) vs[mb][half][i] = ptx::lds32(va + 4 * i);
+          }
+        }
+      // ---- Mask, where some row does not see every token of the tile.
+      const bool edge = base < all_lo || base + TOK > all_hi || live != (1u << MB) - 1;
       if (edge) {
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb)
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int tok = base + mb * 16 + half * 8 + g;
-            const bool here = ((live >> mb) & 1u) != 0u && tok < tile.hi;
+            const bool here = ((live >> mb) & 1u) != 0u;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+              const int r = nt * 8 + 2 * t;
+              if (!here || tok < s_lo[r] || tok >= s_hi[r]) s[mb][nt][half].x = kNegInf;
+              if (!here || tok < s_lo[r + 1] || tok >= s_hi[r + 1]) s[mb][nt][half].y = kNegInf;
+            }
+            // Scales that are not finite, seen or not, do not count here: a
+            // row that sees one has no finite output.
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int r = nt * 8 + 2 * t + j;
-                if (!here || tok < s_lo[r] || tok >= s_hi[r]) s[mb][nt][2 * half + j] = kNegInf;
-              }
-#pragma unroll
-            for (int gi = 0; gi < NG; ++gi) {
-              if (!here) vs[mb][half][gi] = 0u;
-              const uint32_t v = vs[mb][half][gi] & 0x7FFFu;
-              vtop = max(vtop, v < 0x7C00u ? v : 0u);
+            for (int i = 0; i < NG; ++i) {
+              const uint32_t w = vs[mb][half][i];
+              if ((w & 0x7C00u) != 0x7C00u) vbits |= w & 0xFFFFu;
+              if ((w & 0x7C000000u) != 0x7C000000u) vbits |= w >> 16;
             }
           }
       } else {
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb)
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
           for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int gi = 0; gi < NG; ++gi) vtop = max(vtop, vs[mb][half][gi] & 0x7FFFu);
+            for (int i = 0; i < NG; ++i) vbits |= vs[mb][half][i];
+        vbits |= vbits >> 16;
       }
-      // ---- Running maxima, and the exponent of the largest value scale.
-      const int e_tile = static_cast<int>(__reduce_max_sync(0xffffffffu, vtop) >> 10);
-      const int e_new = max(e_run, e_tile);
+      const int e_tile = static_cast<int>((__reduce_or_sync(0xffffffffu, vbits) & 0x7FFFu) >> 10);
+      const int x_new = min(x_run, 29 - e_tile);
+      // ---- Running maxima.
       float mx[NT][2];
-      bool grew = e_new != e_run;
+      bool grew = x_new != x_run;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float x = fmaxf(fmaxf(s[0][nt][j], s[0][nt][2 + j]), fmaxf(s[1][nt][j], s[1][nt][2 + j]));
+          float x = kNegInf;
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+            x = fmaxf(x, j == 0 ? fmaxf(s[mb][nt][0].x, s[mb][nt][1].x) : fmaxf(s[mb][nt][0].y, s[mb][nt][1].y));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -632,92 +688,96 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
           grew = grew || mx[nt][j] != m[nt][j];
         }
       if (__any_sync(0xffffffffu, grew)) {
-        const float shrink = __uint_as_float(static_cast<uint32_t>(127 + e_run - e_new) << 23);
-        e_run = e_new;
+        const float shrink = __uint_as_float(static_cast<uint32_t>(127 + x_new - x_run) << 23);
+        x_run = x_new;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float al[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            al[j] = m[nt][j] == mx[nt][j] ? 1.0f : ex2(m[nt][j] - mx[nt][j]);
-            m[nt][j] = mx[nt][j];
-            l[nt][j] *= al[j];
-            al[j] *= shrink;
-          }
+          float2 al;
+          al.x = m[nt][0] == mx[nt][0] ? 1.0f : ex2((m[nt][0] - mx[nt][0]) * f[nt].x);
+          al.y = m[nt][1] == mx[nt][1] ? 1.0f : ex2((m[nt][1] - mx[nt][1]) * f[nt].y);
+          l[nt] = __fmul2_rn(l[nt], al);
+          m[nt][0] = mx[nt][0];
+          m[nt][1] = mx[nt][1];
+          nmf[nt].x = m[nt][0] == kNegInf ? 0.0f : -m[nt][0] * f[nt].x;
+          nmf[nt].y = m[nt][1] == kNegInf ? 0.0f : -m[nt][1] * f[nt].y;
+          al.x *= shrink;
+          al.y *= shrink;
 #pragma unroll
           for (int c = 0; c < DB; ++c)
 #pragma unroll
-            for (int k2 = 0; k2 < 8; ++k2) o[c][k2 >> 2][nt][k2 & 3] *= al[k2 & 1];
+            for (int k2 = 0; k2 < 8; ++k2) o[c][k2 >> 2][nt][k2 & 3] *= (k2 & 1) ? al.y : al.x;
 #pragma unroll
           for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
-            for (int k2 = 0; k2 < 4; ++k2) zo[gi][nt][k2] *= al[k2 & 1];
+            for (int k2 = 0; k2 < 4; ++k2) zo[gi][nt][k2] *= (k2 & 1) ? al.y : al.x;
         }
       }
+      // ---- P, its sum, and P 2^x_run in fp16 as the B operand of tokens x rows.
+      const float xf = __uint_as_float(static_cast<uint32_t>(127 + x_run) << 23);
+      const float2 xf2 = make_float2(xf, xf);
+      uint32_t pt[MB][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float ref = m[nt][j] == kNegInf ? 0.0f : m[nt][j];
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const float p = ex2(s[mb][nt][2 * half + j] - ref);
-              s[mb][nt][2 * half + j] = p;
-              l[nt][j] += p;
-            }
-        }
-      // ---- O^T += V^T W^T, W = P times the value scales, as fp16.
-      const float wf = __uint_as_float(static_cast<uint32_t>(127 + 29 - e_run) << 23);
-      uint32_t pb[2][NT][2];
+          for (int half = 0; half < 2; ++half) {
+            float2 p = __ffma2_rn(s[mb][nt][half], f[nt], nmf[nt]);
+            p.x = ex2(p.x);
+            p.y = ex2(p.y);
+            l[nt] = __fadd2_rn(l[nt], p);
+            p = __fmul2_rn(p, xf2);
+            pt[mb][nt][half] = transpose8x8(pack_half2(p.x, p.y));
+          }
+      // ---- O^T += V^T W^T with W = P times the value scales, group by group.
+      uint32_t pb[MB][NT][2];
 #pragma unroll
       for (int c = 0; c < DB; ++c) {
         const int gi = c / C::BPG;
         if (c % C::BPG == 0) {
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb)
+          for (int mb = 0; mb < MB; ++mb) {
+            uint32_t z[2] = {0x00080008u, 0x00080008u};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const float w = f16_bits_to_float(vs[mb][half][gi]) * wf;
+              // Scales gi and NG + gi of the words' 2 NG: the two tokens'.
+              constexpr uint32_t kPick[4] = {0x5410u, 0x7610u, 0x5432u, 0x7632u};
+              const uint32_t w = __byte_perm(vs[mb][half][gi / 2], vs[mb][half][(NG + gi) / 2],
+                                             kPick[(gi & 1) * 2 + ((NG + gi) & 1)]);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float w0 = s[mb][nt][2 * half] * w, w1 = s[mb][nt][2 * half + 1] * w;
-                if (edge) {  // a hidden token's weight is 0 under any scale
-                  w0 = s[mb][nt][2 * half] == 0.0f ? 0.0f : w0;
-                  w1 = s[mb][nt][2 * half + 1] == 0.0f ? 0.0f : w1;
-                }
-                pb[mb][nt][half] = transpose8x8(pack_half2(w0, w1));
+              for (int nt = 0; nt < NT; ++nt) pb[mb][nt][half] = mul_half2(pt[mb][nt][half], w);
+              if (edge) {  // a hidden token's weight is 0 under any scale
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  pb[mb][nt][half] = zero_where_zero(pb[mb][nt][half], pt[mb][nt][half]);
+              }
+              if (ASYM) {
+                const uint32_t za = st + C::kZeroAt + C::kZeros + (mb * 16 + half * 8 + 2 * t) * NG + gi;
+                z[half] = lds_u8(za) | (lds_u8(za + NG) << 16);
               }
             }
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb) {
-            uint32_t z0 = 0x00080008u, z1 = 0x00080008u;
-            if (ASYM) {
-              const uint32_t za = st + C::kZeroAt + C::kZeros + (mb * 16 + 2 * t) * NG + gi;
-              z0 = lds_u8(za) | (lds_u8(za + NG) << 16);
-              z1 = lds_u8(za + 8 * NG) | (lds_u8(za + 9 * NG) << 16);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma(zo[gi][nt], z0, z0, z1, z1, pb[mb][nt][0], pb[mb][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma(zo[gi][nt], z[0], z[0], z[1], z[1], pb[mb][nt][0], pb[mb][nt][1]);
           }
         }
-        uint32_t vr[4];
-        ldsm4t(st + C::kCodes + lane * RB + chunk_of<RB>(lane, c) * 16, vr);
+        uint32_t vr[2 * MB];
+#pragma unroll
+        for (int i = 0; i < MB; i += 2)
+          ldsm4t(st + C::kCodes + (i * 16 + lane) * RB + chunk_of<RB>(lane, c) * 16, vr + 2 * i);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t lo[4], hi[4];
+          uint32_t lo[2 * MB], hi[2 * MB];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2 * MB; ++i) {
             lo[i] = pick<ASYM>(vr[i], 0x000F000Fu);
             hi[i] = pick<ASYM>(vr[i], 0x00F000F0u);
             vr[i] >>= 8;
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma(o[c][half][nt], lo[0], hi[0], lo[1], hi[1], pb[0][nt][0], pb[0][nt][1]);
-            mma(o[c][half][nt], lo[2], hi[2], lo[3], hi[3], pb[1][nt][0], pb[1][nt][1]);
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+              mma(o[c][half][nt], lo[2 * mb], hi[2 * mb], lo[2 * mb + 1], hi[2 * mb + 1], pb[mb][nt][0], pb[mb][nt][1]);
         }
       }
     }
@@ -729,10 +789,12 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int o2 = 4; o2 < 32; o2 <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], o2);
-        if (g == 0) {
-          s_m[warp * RT + nt * 8 + 2 * t + j] = m[nt][j];
-          s_l[warp * RT + nt * 8 + 2 * t + j] = l[nt][j];
+        float sum = j == 0 ? l[nt].x : l[nt].y;
+#pragma unroll
+        for (int o2 = 4; o2 < 32; o2 <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
+        if (g == 0) {  // from here on the maxima are S's own
+          s_m[warp * RT + nt * 8 + 2 * t + j] = m[nt][j] * (j == 0 ? f[nt].x : f[nt].y);
+          s_l[warp * RT + nt * 8 + 2 * t + j] = sum;
         }
       }
     const bool whole = n == tile.steps;
@@ -744,12 +806,13 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int r = nt * 8 + 2 * t + j;
+        const float mine = s_m[warp * RT + r];
         float top = s_m[r];
 #pragma unroll
         for (int w = 1; w < kAttnWarps; ++w) top = fmaxf(top, s_m[w * RT + r]);
-        // Codes are 2^-24 times themselves, weights 2^(29 - e_run).
+        // Codes are 2^-24 times themselves, weights 2^x_run.
         const float scale =
-            (m[nt][j] == top ? 1.0f : ex2(m[nt][j] - top)) * __uint_as_float(static_cast<uint32_t>(127 + 24 + e_run - 29) << 23);
+            (mine == top ? 1.0f : ex2(mine - top)) * __uint_as_float(static_cast<uint32_t>(127 + 24 - x_run) << 23);
         float* dst = buf + (warp * 8 + 2 * t + j) * C::kMergePitch + 4 * g;
 #pragma unroll
         for (int c = 0; c < DB; ++c) {
