@@ -297,6 +297,8 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
     __syncthreads();
   }
   if (blockIdx.x == 0 && tid == 0) ws.prefix[0] = 0;
+  // The join may be set up now; it waits for this grid's end before it reads.
+  ptx::launch_dependents();
   const Shares shares(units, ws.blocks);
   if (static_cast<int>(blockIdx.x) >= shares.active) return;
   const int u0 = shares.begin(blockIdx.x);
@@ -888,7 +890,6 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
       tile.set(a, len, count, rt, RT);
     } while (tile.steps == 0);
   }
-  ptx::launch_dependents();
 }
 
 // Joins the pieces of split items and writes the rows that see nothing.  A

@@ -63,6 +63,31 @@ struct Coder {
     u = fminf(fmaxf(u, ASYM ? 0.0f : -8.0f), ASYM ? 15.0f : 7.0f);
     return live ? __float_as_uint(__fadd_rn(u, 12582912.0f)) & 0xFu : 0u;
   }
+  // Eight codes, the first in the lowest nibble; two elements an instruction
+  // (each rounded as by code()) where no quotient is too large.
+  template <bool ASYM>
+  __device__ __forceinline__ void codes8(const float* v, uint32_t& word) const {
+    word = 0u;
+    if (!live) return;
+    if (divide) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) word |= code<ASYM>(v[k]) << (4 * k);
+      return;
+    }
+    const float2 r2 = make_float2(r, r), ns2 = make_float2(-s, -s), z2 = make_float2(z, z);
+    const float2 magic = make_float2(12582912.0f, 12582912.0f);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const float2 x = make_float2(v[k], v[k + 1]);
+      const float2 q = __fmul2_rn(x, r2);
+      float2 u = __ffma2_rn(__ffma2_rn(q, ns2, x), r2, q);
+      if (ASYM) u = __fadd2_rn(u, z2);
+      u.x = fminf(fmaxf(u.x, ASYM ? 0.0f : -8.0f), ASYM ? 15.0f : 7.0f);
+      u.y = fminf(fmaxf(u.y, ASYM ? 0.0f : -8.0f), ASYM ? 15.0f : 7.0f);
+      const float2 t = __fadd2_rn(u, magic);
+      word |= ((__float_as_uint(t.x) & 0xFu) | ((__float_as_uint(t.y) & 0xFu) << 4)) << (4 * k);
+    }
+  }
 };
 
 struct WriteArgs {
@@ -79,6 +104,36 @@ struct ReadArgs {
   const int64_t* slots;
   int64_t tokens;
 };
+
+// A block of the fast kernels takes `per_block` whole tokens, whose 2 H rows
+// are cut into pieces of 16 elements, `per_row` = D / 16 of them: piece i of
+// the block belongs to row i / per_row, row r to token r / (2 H).  Divisions
+// by multiplication with m = ceil(2^32 / divisor), exact for the products
+// below 2^32 that occur (i < 2^16, divisors from 2 to 2^16).
+struct Pieces {
+  uint32_t per_row, per_row_m;
+  uint32_t rows, rows_m;  // 2 H
+  uint32_t per_block;     // tokens
+};
+constexpr int kMaxBlockTokens = 64;
+
+// The cache rows of a block's tokens: that of head 0's key, or -1 where the
+// slot is outside the cache.
+__device__ __forceinline__ void find_rows(const CacheView& c, const int64_t* slots, int64_t token0,
+                                          int64_t tokens, int per_block, int64_t (&rows)[kMaxBlockTokens]) {
+  for (int i = threadIdx.x; i < per_block; i += blockDim.x) {
+    const int64_t slot = token0 + i < tokens ? __ldg(slots + token0 + i) : -1;
+    int64_t row = -1;
+    if (slot >= 0 && slot < c.pages * c.page_size) {
+      // A slot below 2^32 is divided in 32 bits.
+      const int64_t page = slot < (1LL << 32) ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(c.page_size)
+                                              : slot / c.page_size;
+      row = c.row(page, 0, 0, slot - page * c.page_size);
+    }
+    rows[i] = row;
+  }
+  __syncthreads();
+}
 
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8]);
@@ -110,36 +165,41 @@ __device__ __forceinline__ void load8<__half>(const __half* p, float (&v)[8]) {
   }
 }
 
-// D a multiple of 8, group = 8 LPG dividing D with LPG a power of two <= 32,
-// every source row 16-byte aligned, packed 4-byte aligned.  A thread codes 8
-// consecutive elements of one row (one 16-byte load of 16-bit elements, one
-// 4-byte store); the LPG lanes of a group find its extremes with shuffles.
-// A block takes `per_block` whole tokens; `chunks` = 2 H D / 8 of a token.
+// D a multiple of 16, group = 16 LPG dividing D with LPG a power of two <= 32,
+// every source row 16-byte aligned, packed 8-byte aligned.  A thread codes 16
+// consecutive elements of one row (two 16-byte loads of 16-bit elements, one
+// 8-byte store); the LPG lanes of a group, neighbours in one warp since LPG
+// divides D / 16, find its extremes with shuffles.
 template <typename T, bool ASYM>
 __global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant__ WriteArgs a,
-                                                          int chunks, int per_block, int lpg) {
+                                                          const Pieces p, const int lpg) {
   const CacheView& c = a.cache;
-  const int per_row = c.head_dim >> 3;
-  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * per_block;
-  const int total = per_block * chunks;
+  __shared__ int64_t s_rows[kMaxBlockTokens];
+  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * p.per_block;
+  find_rows(c, a.slots, token0, a.tokens, p.per_block, s_rows);
+  const uint32_t total = p.per_block * p.rows * p.per_row;
   // Whole warps take part in every step, so that the shuffles are uniform.
-  for (int base = 0; base < total; base += blockDim.x) {
-    const int i = base + threadIdx.x;
-    const int64_t t = token0 + i / chunks;
-    bool live = i < total && t < a.tokens;
-    int64_t slot = live ? __ldg(a.slots + t) : -1;
-    live = slot >= 0 && slot < c.pages * c.page_size;
-    const int chunk = i % chunks;
-    const int row = chunk / per_row;  // kv * H + h
-    const int d = (chunk - row * per_row) * 8;
-    const int kv = row >= c.heads ? 1 : 0;
+  for (uint32_t base = 0; base < total; base += blockDim.x) {
+    const uint32_t i = base + threadIdx.x;
+    const uint32_t r = __umulhi(i, p.per_row_m), d = (i - r * p.per_row) * 16;
+    const uint32_t tok = __umulhi(r, p.rows_m), row = r - tok * p.rows;
+    const int64_t at0 = i < total ? s_rows[tok] : -1;
+    const int kv = row >= static_cast<uint32_t>(c.heads) ? 1 : 0;
     const int h = row - kv * c.heads;
-    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (live)
-      load8<T>(static_cast<const T*>(a.src[kv]) + t * a.token_stride[kv] + h * a.head_stride[kv] + d, v);
+    float v[16];
+    if (at0 >= 0) {
+      const T* src = static_cast<const T*>(kv ? a.src[1] : a.src[0]) +
+                     (token0 + tok) * (kv ? a.token_stride[1] : a.token_stride[0]) +
+                     h * (kv ? a.head_stride[1] : a.head_stride[0]) + d;
+      load8<T>(src, *reinterpret_cast<float(*)[8]>(v));
+      load8<T>(src + 8, *reinterpret_cast<float(*)[8]>(v + 8));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+    }
     float lo = ASYM ? v[0] : 0.0f, hi = ASYM ? v[0] : fabsf(v[0]);
 #pragma unroll
-    for (int k = 1; k < 8; ++k) {
+    for (int k = 1; k < 16; ++k) {
       if (ASYM) lo = fminf(lo, v[k]);
       hi = fmaxf(hi, ASYM ? v[k] : fabsf(v[k]));
     }
@@ -147,14 +207,14 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant_
       if (ASYM) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
     }
-    if (!live) continue;
+    if (at0 < 0) continue;
     Coder q;
     q.set<ASYM>(lo, hi);
-    uint32_t word = 0u;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) word |= q.code<ASYM>(v[k]) << (4 * k);
-    const int64_t at = c.row(slot / c.page_size, kv, h, slot % c.page_size);
-    *reinterpret_cast<uint32_t*>(c.packed + at * c.row_bytes + (d >> 1)) = word;
+    uint2 word = make_uint2(0u, 0u);
+    q.codes8<ASYM>(v, word.x);
+    q.codes8<ASYM>(v + 8, word.y);
+    const int64_t at = at0 + static_cast<int64_t>(row) * c.page_size;  // values follow the keys of all heads
+    *reinterpret_cast<uint2*>(c.packed + at * c.row_bytes + (d >> 1)) = word;
     if ((threadIdx.x & (lpg - 1)) == 0) {
       const int64_t g = at * c.groups + d / c.group;
       c.scales[g] = q.bits;
@@ -246,36 +306,46 @@ __device__ __forceinline__ void store8<__half>(__half* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// D and group multiples of 8, packed 4-byte and outputs 16-byte aligned: a
-// thread gives 8 consecutive elements of one row.
+// D and group multiples of 16, packed 8-byte and outputs 16-byte aligned: a
+// thread gives 16 consecutive elements of one row (one 8-byte load, two
+// 16-byte stores of 16-bit elements).
 template <typename TO, bool ASYM>
-__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ ReadArgs a, int chunks,
-                                                         int per_block) {
+__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ ReadArgs a, const Pieces p) {
   const CacheView& c = a.cache;
-  const int per_row = c.head_dim >> 3;
-  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * per_block;
-  const int total = per_block * chunks;
-  for (int i = threadIdx.x; i < total; i += blockDim.x) {
-    const int64_t t = token0 + i / chunks;
-    if (t >= a.tokens) return;
-    const int64_t slot = __ldg(a.slots + t);
-    const int chunk = i % chunks;
-    const int row = chunk / per_row;
-    const int d = (chunk - row * per_row) * 8;
-    const int kv = row >= c.heads ? 1 : 0;
+  __shared__ int64_t s_rows[kMaxBlockTokens];
+  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * p.per_block;
+  find_rows(c, a.slots, token0, a.tokens, p.per_block, s_rows);
+  const int64_t here = a.tokens - token0;
+  const uint32_t total = (here < p.per_block ? static_cast<uint32_t>(here) : p.per_block) * p.rows * p.per_row;
+#pragma unroll 4
+  for (uint32_t i = threadIdx.x; i < total; i += blockDim.x) {
+    const uint32_t r = __umulhi(i, p.per_row_m), d = (i - r * p.per_row) * 16;
+    const uint32_t tok = __umulhi(r, p.rows_m), row = r - tok * p.rows;
+    const int64_t at0 = s_rows[tok];
+    const int kv = row >= static_cast<uint32_t>(c.heads) ? 1 : 0;
     const int h = row - kv * c.heads;
-    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (slot >= 0 && slot < c.pages * c.page_size) {
-      const int64_t at = c.row(slot / c.page_size, kv, h, slot % c.page_size);
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(c.packed + at * c.row_bytes + (d >> 1)));
+    const int64_t at = at0 + static_cast<int64_t>(row) * c.page_size;
+    uint2 w = make_uint2(0u, 0u);
+    float s = 0.0f;
+    int zp = 0;
+    if (at0 >= 0) {
+      w = __ldg(reinterpret_cast<const uint2*>(c.packed + at * c.row_bytes + (d >> 1)));
       const int64_t g = at * c.groups + d / c.group;
-      const float s = f16_bits_to_float(__ldg(c.scales + g));
-      const int zp = ASYM ? static_cast<int>(__ldg(c.zeros + g)) : 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = code_value<ASYM>((w >> (4 * k)) & 0xFu, zp) * s;
+      s = f16_bits_to_float(__ldg(c.scales + g));
+      if (ASYM) zp = static_cast<int>(__ldg(c.zeros + g));
     }
-    TO* out = static_cast<TO*>(a.dst[kv]) + (t * c.heads + h) * c.head_dim + d;
-    store8<TO>(out, v);
+    TO* out = static_cast<TO*>(kv ? a.dst[1] : a.dst[0]) + ((token0 + tok) * c.heads + h) * c.head_dim + d;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = code_value<ASYM>(((half ? w.y : w.x) >> (4 * k)) & 0xFu, zp) * s;
+      if (at0 < 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+      }
+      store8<TO>(out + 8 * half, v);
+    }
   }
 }
 
@@ -315,49 +385,52 @@ __global__ void __launch_bounds__(256) cache_read_any_kernel(const __grid_consta
 
 bool multiple_of(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// The blocks of a fast kernel: about four pieces a thread, fewer where that
+// would leave SMs without a block.  False where the sizes are out of its range.
+bool cut(const CacheView& c, int64_t tokens, Pieces* p, int64_t* grid) {
+  const int64_t per_row = c.head_dim / 16, rows = 2LL * c.heads;
+  if (c.head_dim % 16 != 0 || c.group % 16 != 0 || per_row < 2 || rows * per_row > 8192) return false;
+  int64_t n = 1024 / (rows * per_row);
+  const int64_t spread = (tokens + 4 * num_sms() - 1) / (4 * num_sms());
+  n = n < spread ? n : spread;
+  n = n < 1 ? 1 : (n < kMaxBlockTokens ? n : kMaxBlockTokens);
+  *p = {static_cast<uint32_t>(per_row), static_cast<uint32_t>(((1LL << 32) + per_row - 1) / per_row),
+        static_cast<uint32_t>(rows), static_cast<uint32_t>(((1LL << 32) + rows - 1) / rows), static_cast<uint32_t>(n)};
+  *grid = (tokens + n - 1) / n;
+  return *grid <= 0x7FFFFFFF;
+}
+
 template <typename T, bool ASYM>
 cudaError_t write_typed(const WriteArgs& a, cudaStream_t stream) {
   const CacheView& c = a.cache;
-  const int lpg = c.group / 8;
-  const int64_t chunks = 2LL * c.heads * (c.head_dim / 8);
-  bool fast = c.head_dim % 8 == 0 && c.group % 8 == 0 && lpg <= 32 && (lpg & (lpg - 1)) == 0 &&
-              c.head_dim % c.group == 0 && multiple_of(c.packed, 4) && chunks <= (1 << 20);
+  const int lpg = c.group / 16;
+  Pieces p;
+  int64_t grid;
+  bool fast = cut(c, a.tokens, &p, &grid) && lpg <= 32 && (lpg & (lpg - 1)) == 0 && c.head_dim % c.group == 0 &&
+              multiple_of(c.packed, 8);
   for (int kv = 0; kv < 2; ++kv)
     fast = fast && multiple_of(a.src[kv], 16) && (a.token_stride[kv] * sizeof(T)) % 16 == 0 &&
            (a.head_stride[kv] * sizeof(T)) % 16 == 0;
   if (fast) {
-    const int per_block = chunks >= 256 ? 1 : static_cast<int>(256 / chunks);
-    const int64_t grid = (a.tokens + per_block - 1) / per_block;
-    if (grid <= 0x7FFFFFFF) {
-      cache_write_kernel<T, ASYM><<<static_cast<unsigned>(grid), 256, 0, stream>>>(
-          a, static_cast<int>(chunks), per_block, lpg);
-      return cudaGetLastError();
-    }
+    cache_write_kernel<T, ASYM><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a, p, lpg);
+    return cudaGetLastError();
   }
   const int64_t warps = a.tokens * 2 * c.heads;
-  const int grid = resident_grid(cache_write_any_kernel<T, ASYM>, (warps + 7) / 8);
-  cache_write_any_kernel<T, ASYM><<<grid, 256, 0, stream>>>(a);
+  cache_write_any_kernel<T, ASYM><<<resident_grid(cache_write_any_kernel<T, ASYM>, (warps + 7) / 8), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 template <typename TO, bool ASYM>
 cudaError_t read_typed(const ReadArgs& a, cudaStream_t stream) {
   const CacheView& c = a.cache;
-  const int64_t chunks = 2LL * c.heads * (c.head_dim / 8);
-  const bool fast = c.head_dim % 8 == 0 && c.group % 8 == 0 && multiple_of(c.packed, 4) &&
-                    multiple_of(a.dst[0], 16) && multiple_of(a.dst[1], 16) && chunks <= (1 << 20);
-  if (fast) {
-    const int per_block = chunks >= 256 ? 1 : static_cast<int>(256 / chunks);
-    const int64_t grid = (a.tokens + per_block - 1) / per_block;
-    if (grid <= 0x7FFFFFFF) {
-      cache_read_kernel<TO, ASYM><<<static_cast<unsigned>(grid), 256, 0, stream>>>(
-          a, static_cast<int>(chunks), per_block);
-      return cudaGetLastError();
-    }
+  Pieces p;
+  int64_t grid;
+  if (cut(c, a.tokens, &p, &grid) && multiple_of(c.packed, 8) && multiple_of(a.dst[0], 16) && multiple_of(a.dst[1], 16)) {
+    cache_read_kernel<TO, ASYM><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a, p);
+    return cudaGetLastError();
   }
   const int64_t bytes = a.tokens * 2 * c.heads * c.row_bytes;
-  const int grid = resident_grid(cache_read_any_kernel<TO, ASYM>, (bytes + 255) / 256);
-  cache_read_any_kernel<TO, ASYM><<<grid, 256, 0, stream>>>(a);
+  cache_read_any_kernel<TO, ASYM><<<resident_grid(cache_read_any_kernel<TO, ASYM>, (bytes + 255) / 256), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
