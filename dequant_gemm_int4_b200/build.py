@@ -2,7 +2,9 @@
 
 Usage: ``python -m dequant_gemm_int4_b200.build`` (or ``build()`` from Python).
 Object files go to ``dequant_gemm_int4_b200/_build/``; the shared library is
-written next to this file so that it travels with the source tree.
+written next to this file so that it travels with the source tree, and beside
+it ``_cache_binding.so``, the CPython extension (C++ against torch's headers,
+no device code) through which ``cache.py`` calls it.
 """
 
 from __future__ import annotations
@@ -17,6 +19,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libint4.so")
+BINDING_SRC = os.path.join(PKG, "cache_binding.cpp")
+BINDING = os.path.join(PKG, "_cache_binding.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -61,12 +65,38 @@ def _compile(nvcc: str, src: str, extra: list[str], verbose: bool) -> str:
     return obj
 
 
+def _build_binding(verbose: bool = False) -> None:
+    """Compile cache_binding.cpp into the extension module _cache_binding.so."""
+    import sysconfig
+
+    import torch
+
+    headers = [os.path.join(INCLUDE, "int4.h"), torch.__file__]
+    if not _stale(BINDING, [BINDING_SRC] + headers):
+        return
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    cmd = [cxx, "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + INCLUDE, "-I" + sysconfig.get_path("include"), "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", BINDING,
+           "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed on {os.path.basename(BINDING_SRC)}:\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile every .cu under csrc/ and link libint4.so; returns its path."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     srcs = sources()
+    binding = concurrent.futures.ThreadPoolExecutor(max_workers=1).submit(_build_binding, verbose)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(nvcc, s, extra, verbose or ptxas_info), srcs))
     if _stale(LIB, objs) or ptxas_info:
@@ -76,6 +106,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    binding.result()
     return LIB
 
 

@@ -12,7 +12,15 @@ import torch
 import dequant_gemm_int4_b200 as q4
 from cache_util import attention_ref, code_rows, random_cache, value_rows
 from dequant_gemm_int4_b200 import build as q4build
-from dequant_gemm_int4_b200.cache import _Cache
+
+
+class _Cache(ctypes.Structure):
+    """int4_cache of include/int4.h."""
+
+    _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("group", ctypes.c_int32)]
+
 
 FAKE = 256  # an address that is never dereferenced: validation fails first
 
