@@ -140,8 +140,6 @@ cudaError_t launch_any_typed(const AttentionArgs& a, cudaStream_t stream) {
 
 bool multiple_of(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
-
 }  // namespace
 
 cudaError_t launch_cache_attention_any(const AttentionArgs& a, DType t, cudaStream_t stream) {
@@ -175,6 +173,18 @@ bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out,
          multiple_of(c.zeros, 16) && multiple_of(out, 8);
 }
 
+// The tcgen05 kernel takes heads of 64 or 128 elements in one group, and
+// outputs aligned to 16 bytes.
+bool cache_prefill_supported(const CacheView& c, DType t, const void* out, int64_t rows, int64_t batch, int ratio,
+                             int64_t max_pages) {
+  return (c.head_dim == 64 || c.head_dim == 128) && c.group == c.head_dim && multiple_of(out, 16) &&
+         cache_attention_mma_supported(c, t, out, rows, batch, ratio, max_pages);
+}
+
+size_t cache_prefill_workspace(const CacheView& c, int64_t batch) {
+  return attention_space_bytes(batch, num_sms(), cache_prefill_row_tile(), c.head_dim);
+}
+
 size_t cache_attention_mma_workspace(const CacheView& c, int64_t rows, int64_t batch, int ratio) {
   const int rt = attention_row_tile(c.head_dim, rows, batch, ratio);
   const bool asym = c.zeros != nullptr;
@@ -185,8 +195,7 @@ size_t cache_attention_mma_workspace(const CacheView& c, int64_t rows, int64_t b
     case 128: blocks = cache_attention_blocks_128(c.group, asym, rt); break;
     default: blocks = cache_attention_blocks_256(c.group, asym, rt); break;
   }
-  return attention_prefix_bytes(batch) +
-         round_up(static_cast<size_t>(2) * blocks * rt * (c.head_dim + 2) * sizeof(float), 256);
+  return attention_space_bytes(batch, blocks, rt, c.head_dim);
 }
 
 cudaError_t launch_cache_attention_mma(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream) {

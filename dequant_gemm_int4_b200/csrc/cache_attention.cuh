@@ -203,6 +203,11 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // Halves of r are zeroed where those of p are zero.
 __device__ __forceinline__ uint32_t zero_where_zero(uint32_t r, uint32_t p) {
   if ((p & 0x7FFFu) == 0u) r &= 0xFFFF0000u;
@@ -610,10 +615,9 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
         }
       }
       // ---- Value scales of tokens 2t, 2t + 1 of each group of 8: NG words
-      // hold the two tokens' scales; x_new follows their largest exponent
-      // (the OR of the bits bounds it, by less than twice).
+      // hold the two tokens' scales; x_new follows the largest one's exponent.
       uint32_t vs[MB][2][NG];
-      uint32_t vbits = 0u;
+      uint32_t vtop = 0u;
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -657,8 +661,8 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
               const uint32_t w = vs[mb][half][i];
-              if ((w & 0x7C00u) != 0x7C00u) vbits |= w & 0xFFFFu;
-              if ((w & 0x7C000000u) != 0x7C000000u) vbits |= w >> 16;
+              vtop = attn::max_half2(vtop, ((w & 0x7C00u) != 0x7C00u ? w & 0xFFFFu : 0u) |
+                                               ((w & 0x7C000000u) != 0x7C000000u ? w & 0xFFFF0000u : 0u));
             }
           }
       } else {
@@ -667,10 +671,9 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
 #pragma unroll
           for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int i = 0; i < NG; ++i) vbits |= vs[mb][half][i];
-        vbits |= vbits >> 16;
+            for (int i = 0; i < NG; ++i) vtop = attn::max_half2(vtop, vs[mb][half][i]);
       }
-      const int e_tile = static_cast<int>((__reduce_or_sync(0xffffffffu, vbits) & 0x7FFFu) >> 10);
+      const int e_tile = static_cast<int>(__reduce_max_sync(0xffffffffu, max(vtop & 0xFFFFu, vtop >> 16)) >> 10);
       const int x_new = min(x_run, 29 - e_tile);
       // ---- Running maxima.
       float mx[NT][2];
@@ -1013,29 +1016,24 @@ inline int attention_row_tile(int head_dim, int64_t rows, int64_t batch, int rat
   return r <= 16 || head_dim > 128 ? 16 : 32;
 }
 
-template <class C>
-int attention_blocks() {
-  return num_sms() * C::kBlocks;
+// The parts of a workspace.
+inline AttentionSpace attention_space(void* workspace, int batch, int blocks, int rt, int head_dim) {
+  AttentionSpace ws;
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  ws.blocks = blocks;
+  ws.prefix = reinterpret_cast<int32_t*>(p);
+  ws.o = reinterpret_cast<float*>(p + attention_prefix_bytes(batch));
+  ws.ml = ws.o + 2LL * blocks * rt * head_dim;
+  return ws;
+}
+inline size_t attention_space_bytes(int64_t batch, int64_t blocks, int rt, int head_dim) {
+  return attention_prefix_bytes(batch) + (2 * blocks * rt * (head_dim + 2) * sizeof(float) + 255) / 256 * 256;
 }
 
-template <typename T, class C>
-cudaError_t launch_attention_cfg(const AttentionArgs& a, void* workspace, cudaStream_t stream) {
-  AttentionSpace ws;
-  ws.blocks = attention_blocks<C>();
-  uint8_t* p = static_cast<uint8_t*>(workspace);
-  ws.prefix = reinterpret_cast<int32_t*>(p);
-  p += attention_prefix_bytes(a.batch);
-  ws.o = reinterpret_cast<float*>(p);
-  ws.ml = ws.o + 2LL * ws.blocks * C::RT * C::D;
-  auto kernel = attention_mma_kernel<T, C>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
-  int shift = 0;
-  while ((1 << shift) < a.cache.page_size) ++shift;
-  kernel<<<ws.blocks, kAttnThreads, C::kSmem, stream>>>(a, ws, shift);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // The join starts while the last shares are finished.
+// The join, launched early where the kernel before it lets it (it waits for
+// that kernel's end before it reads).
+template <typename T>
+cudaError_t launch_attention_join(const AttentionArgs& a, const AttentionSpace& ws, int rt, cudaStream_t stream) {
   const int rows = a.rows * a.q_heads;
   const int wpr = rows <= 2048 ? 8 : 1;
   cudaLaunchConfig_t cfg = {};
@@ -1047,7 +1045,26 @@ cudaError_t launch_attention_cfg(const AttentionArgs& a, void* workspace, cudaSt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T>, a, ws, C::RT, wpr);
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T>, a, ws, rt, wpr);
+}
+
+template <class C>
+int attention_blocks() {
+  return num_sms() * C::kBlocks;
+}
+
+template <typename T, class C>
+cudaError_t launch_attention_cfg(const AttentionArgs& a, void* workspace, cudaStream_t stream) {
+  const AttentionSpace ws = attention_space(workspace, a.batch, attention_blocks<C>(), C::RT, C::D);
+  auto kernel = attention_mma_kernel<T, C>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  int shift = 0;
+  while ((1 << shift) < a.cache.page_size) ++shift;
+  kernel<<<ws.blocks, kAttnThreads, C::kSmem, stream>>>(a, ws, shift);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_attention_join<T>(a, ws, C::RT, stream);
 }
 
 // Calls f with the configuration for a cache and row tile; false if none.

@@ -1,0 +1,749 @@
+// Attention over the 4-bit cache for many query rows (prompts in chunks), on
+// the tcgen05 tensor cores (sm_100a).
+//
+// Same operator, split over the lengths and joining kernel as the kernel for
+// few rows (cache_attention.cuh); here a block's item is 256 query rows of one
+// key/value head, two MMA tiles of 128 rows that share every key and value
+// tile of 128 tokens:
+//   S_m = Q_m K^T         128 x 128 x D, both operands in shared memory
+//   O_m += W_m V          128 x D x 128, W from tensor memory
+// Tensor memory holds S_0, S_1 (fp32, 128 columns each; W_m, fp16, overlays the
+// first half of S_m once S_m has been read) and O_0, O_1 (D columns each).
+//
+// Roles of the block's 16 warps:
+//   warps 0-3    warp 0 issues the MMAs; the others only lend their registers
+//   warps 4-7    expand codes: thread t owns token t of the tile, its key row
+//                and its value row
+//   warps 8-15   softmax: thread r of group m owns query row r of tile m
+// The issue order S_0(j+1) behind W_0(j) V, S_1(j+1) behind W_1(j) V lets each
+// group's softmax run under the other group's MMAs.
+//
+// Operands are exact: q in fp16 after a power-of-two scaling of its row (see
+// cache_attention.cuh), keys and values as the integers n - z.  The token's
+// key scale multiplies its column of S in fp32, its value scale the weight,
+// W = 2^x P s rounded to fp16 once (x: a power of two that keeps it in range).
+// So one group a head is required here (group = head_dim).  S, the maximum and
+// the sum are fp32; O is fp32 in tensor memory, rescaled only when a row's
+// maximum has grown by more than 2^8 (weights may reach 2^8 until then).
+//
+// Inside blocks of 8 elements, keys and queries are stored in the order 0, 4,
+// 1, 5, 2, 6, 3, 7 in which a code word expands pair by pair; O's columns come
+// out in that order and are put right when they are stored.
+#include <type_traits>
+
+#include "cache.cuh"
+#include "cache_attention.cuh"
+#include "internal.h"
+#include "sm100_ptx.cuh"
+
+namespace int4lib {
+
+namespace {
+
+constexpr int kRows = 256;     // query rows of an item
+constexpr int kTok = 128;      // tokens of a tile
+constexpr int kThreadsP = 512;
+constexpr int kScaleRing = 4;  // tiles of column scales held
+constexpr float kGrow = 8.0f;  // log2 of how far a weight may pass the maximum it is relative to
+constexpr uint64_t kWaitNs = 250000000ull;  // far above any legitimate wait
+
+struct Bars {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t sc_full[kScaleRing];
+  uint64_t s_full[2], w_full[2];  // per row tile: S computed; W stored
+  uint64_t q_full, o_full;        // per item
+  uint64_t drain;
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kSub = 128 * 128;         // 128 rows of 128 bytes: 64 elements, 128-byte swizzle
+  static constexpr int kTile = D / 64 * kSub;    // 128 rows of D elements
+  static constexpr int offQ = 0;                 // two row tiles
+  static constexpr int offK = offQ + 2 * kTile;  // two stages
+  static constexpr int offV = offK + 2 * kTile;  // two stages
+  static constexpr int offScale = offV + 2 * kTile;             // [ring][key, value][128] fp32
+  static constexpr int offBits = offScale + kScaleRing * 2 * kTok * 4;  // [ring][4 + 4]: live tokens, largest value scales
+  static constexpr int offBar = offBits + kScaleRing * 8 * 4;
+  static constexpr int offMisc = offBar + static_cast<int>(sizeof(Bars));
+  static constexpr int kAlloc = offMisc + 64 + 1024;  // slack to align the base to 1024
+};
+
+// Operand stored with rows along K and 128-byte swizzle, read with its
+// contiguous dimension along N: 8 rows of an atom `8 * 128` bytes apart along
+// K (stride offset), atoms of 64 elements kSub bytes apart along N (leading
+// offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t atom_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(atom_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16, one CTA.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// fp16 operands, fp32 result, M = 128; n_major: B contiguous along N.
+__device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool n_major) {
+  return (1u << 4) | (n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+struct Wait {
+  volatile uint32_t* abort;
+  uint32_t* status;
+};
+// Bounded wait for a barrier's phase: false when the block is giving up.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const Wait& w) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  for (uint32_t i = 1; i != 0; ++i) {
+    if (ptx::mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    if ((i & 15u) == 0u) {
+      if (*w.abort) return false;
+      if (ptx::globaltimer() - t0 > kWaitNs) break;
+    }
+  }
+  *w.abort = 1u;
+  report_status(w.status, kStatusTimeout);
+  return false;
+}
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Wait& w) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, w));
+}
+
+// A code word as 8 fp16 integers n - z in the order 0 4 1 5 2 6 3 7: with
+// n in a half's low bits under the exponent of 1024 it is 1024 + n, four bits
+// up 1024 + 16 n.  b1 = -(1024 + z) and b16 = -(64 + z) in both halves.
+template <bool ASYM>
+__device__ __forceinline__ uint4 expand(uint32_t w, uint32_t b1, uint32_t b16) {
+  // (w & mask) | 0x64006400, with the sign bit of two's-complement codes
+  // flipped (n - 8): 0x6a = (a & b) ^ c.
+  constexpr uint32_t k1 = ASYM ? 0x64006400u : 0x64086408u, k16 = ASYM ? 0x64006400u : 0x64806480u;
+  uint32_t x[4], o[4];
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(x[0]) : "r"(w), "r"(0x000F000Fu), "r"(k1));
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(x[1]) : "r"(w), "r"(0x00F000F0u), "r"(k16));
+  w >>= 8;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(x[2]) : "r"(w), "r"(0x000F000Fu), "r"(k1));
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(x[3]) : "r"(w), "r"(0x00F000F0u), "r"(k16));
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(x[i]), "r"(b1));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[i + 1]) : "r"(x[i + 1]), "r"(0x2C002C00u), "r"(b16));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <typename T, int D, bool ASYM>
+__global__ void __launch_bounds__(kThreadsP, 1)
+    attention_prefill_kernel(const __grid_constant__ AttentionArgs a, const AttentionSpace ws, const int page_shift,
+                             uint32_t* status) {
+  using L = Smem<D>;
+  constexpr float kNegInf = -__builtin_huge_valf();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                   ~static_cast<uintptr_t>(1023));
+  const CacheView& cache = a.cache;
+  Bars* const bars = reinterpret_cast<Bars*>(smem + L::offBar);
+  uint32_t* const misc = reinterpret_cast<uint32_t*>(smem + L::offMisc);  // TMEM address, abort flag, plan
+  volatile uint32_t* const abort_flag = misc + 1;
+  int* const s_plan = reinterpret_cast<int*>(misc + 2);  // sequence, offset; then scan[4]
+  float* const s_scale = reinterpret_cast<float*>(smem + L::offScale);
+  volatile uint32_t* const s_bits = reinterpret_cast<volatile uint32_t*>(smem + L::offBits);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto bar = [&](uint64_t& b) { return ptx::smem_u32(&b); };
+  const Wait wc{abort_flag, status};
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(bars->k_full[i]), 4);
+      ptx::mbar_init(bar(bars->k_empty[i]), 1);
+      ptx::mbar_init(bar(bars->v_full[i]), 4);
+      ptx::mbar_init(bar(bars->v_empty[i]), 1);
+      ptx::mbar_init(bar(bars->s_full[i]), 1);
+      ptx::mbar_init(bar(bars->w_full[i]), 4);
+    }
+    for (int i = 0; i < kScaleRing; ++i) ptx::mbar_init(bar(bars->sc_full[i]), 4);
+    ptx::mbar_init(bar(bars->q_full), 8);
+    ptx::mbar_init(bar(bars->o_full), 1);
+    ptx::mbar_init(bar(bars->drain), 1);
+    *abort_flag = 0u;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(misc), 512);
+    ptx::tmem_relinquish();
+  }
+
+  // ---- This block's share (as in attention_mma_kernel; the first 128 threads).
+  int units = 0;
+  {
+    int mine = 0, upto = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 128) {
+      const int b = b0 + tid;
+      if (tid < 128) {
+        mine = b < a.batch ? head_units(a, b, kRows) * cache.heads : 0;
+        upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        if (lane == 31) s_plan[2 + warp] = upto;
+      }
+      __syncthreads();
+      int all = 0;
+      for (int w = 0; w < 4; ++w) {
+        if (w < warp) upto += s_plan[2 + w];
+        all += s_plan[2 + w];
+      }
+      if (blockIdx.x == 0 && tid < 128 && b < a.batch) ws.prefix[b + 1] = units + upto;
+      units += all;
+      __syncthreads();
+    }
+    if (blockIdx.x == 0 && tid == 0) ws.prefix[0] = 0;
+  }
+  const Shares shares(units, ws.blocks);
+  const bool working = static_cast<int>(blockIdx.x) < shares.active;
+  const int u0 = working ? shares.begin(blockIdx.x) : 0;
+  const int my_units = working ? shares.begin(blockIdx.x + 1) - u0 : 0;
+  if (working) {
+    int before = 0;
+    for (int b0 = 0; b0 < a.batch && before <= u0; b0 += 128) {  // the same for every thread
+      const int b = b0 + tid;
+      int mine = 0, upto = 0;
+      if (tid < 128) {
+        mine = b < a.batch ? head_units(a, b, kRows) * cache.heads : 0;
+        upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        if (lane == 31) s_plan[2 + warp] = upto;
+      }
+      __syncthreads();
+      int all = 0;
+      for (int w = 0; w < 4; ++w) {
+        if (w < warp) upto += s_plan[2 + w];
+        all += s_plan[2 + w];
+      }
+      upto += before;
+      if (tid < 128 && upto - mine <= u0 && u0 < upto) {
+        s_plan[0] = b;
+        s_plan[1] = u0 - (upto - mine);
+      }
+      before += all;
+      __syncthreads();
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = misc[0];
+
+  // ---- The walk over the share's items, the same in every role.
+  struct Walk {
+    int b, h, rt, n_rt, first, count, len, s0, left;
+    RowTile tile;
+    __device__ __forceinline__ void start(const AttentionArgs& a, int b_, int off, int units_) {
+      b = b_;
+      left = units_;
+      if (left == 0) return;
+      a.queries(b, first, count);
+      len = a.kv_len(b);
+      n_rt = row_tiles(a, count, kRows);
+      const int per_head = head_units(a, b, kRows);
+      h = off / per_head;
+      off -= h * per_head;
+      rt = 0;
+      tile.set(a, len, count, 0, kRows);
+      while (off >= tile.steps) {
+        off -= tile.steps;
+        tile.set(a, len, count, ++rt, kRows);
+      }
+      s0 = off;
+    }
+    __device__ __forceinline__ int steps() const { return min(left, tile.steps - s0); }
+    __device__ __forceinline__ void next(const AttentionArgs& a) {
+      left -= steps();
+      if (left == 0) return;
+      s0 = 0;
+      do {
+        if (++rt == n_rt) {
+          rt = 0;
+          if (++h == a.cache.heads) {
+            h = 0;
+            do {
+              ++b;
+              a.queries(b, first, count);
+              len = a.kv_len(b);
+              n_rt = row_tiles(a, count, kRows);
+            } while (n_rt == 0);
+          }
+        }
+        tile.set(a, len, count, rt, kRows);
+      } while (tile.steps == 0);
+    }
+  };
+  Walk w;
+
+  // Registers a thread: 40 for the MMA warps, 88 for the expanders, 192 for
+  // the softmax; 128 * 40 + 128 * 88 + 256 * 192 = 65536 = 512 * 128, what the
+  // block is launched with.
+  if (warp < 4) {
+    ptx::regs_dec<40>();
+    if (warp == 0) {
+      // ---------------- MMA issuer ----------------
+      w.start(a, s_plan[0], s_plan[1], my_units);
+      const bool leader = ptx::elect_one();
+      constexpr uint32_t id_s = instr_desc(kTok, false), id_o = instr_desc(D, true);
+      const uint32_t q_at = ptx::smem_u32(smem + L::offQ), k_at = ptx::smem_u32(smem + L::offK),
+                     v_at = ptx::smem_u32(smem + L::offV);
+      auto s_mma = [&](int m, int stage) {
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * L::kSub + (k % 4) * 32;
+            ptx::umma_f16(tmem + m * kTok, ptx::sw128_kmajor_desc(q_at + m * L::kTile + off),
+                          ptx::sw128_kmajor_desc(k_at + stage * L::kTile + off), id_s, k == 0 ? 0u : 1u);
+          }
+          ptx::umma_commit(bar(bars->s_full[m]));
+        }
+        __syncwarp();
+      };
+      auto o_mma = [&](int m, int stage, bool first) {
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < kTok / 16; ++k)
+            umma_f16_ts(tmem + 2 * kTok + m * D, tmem + m * kTok + 8 * k,
+                        sw128_mnmajor_desc(v_at + stage * L::kTile + k * 2048, L::kSub), id_o,
+                        first && k == 0 ? 0u : 1u);
+        }
+        __syncwarp();
+      };
+      int t = 0;  // tiles before this one
+      uint32_t item = 0;
+      bool ok = true;
+      while (ok && w.left > 0) {
+        const int n = w.steps();
+        ok = wait_all(bar(bars->q_full), item & 1u, wc) && wait_all(bar(bars->k_full[t & 1]), (t >> 1) & 1u, wc);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        s_mma(0, t & 1);
+        s_mma(1, t & 1);
+        if (leader) ptx::umma_commit(bar(bars->k_empty[t & 1]));
+        __syncwarp();
+        for (int j = 0; ok && j < n; ++j, ++t) {
+          ok = wait_all(bar(bars->v_full[t & 1]), (t >> 1) & 1u, wc);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            ok = ok && wait_all(bar(bars->w_full[m]), t & 1u, wc);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            o_mma(m, t & 1, j == 0);
+            if (j + 1 < n) {
+              if (m == 0) {
+                ok = wait_all(bar(bars->k_full[(t + 1) & 1]), ((t + 1) >> 1) & 1u, wc);
+                if (!ok) break;
+                ptx::tc_fence_after();
+              }
+              s_mma(m, (t + 1) & 1);
+            }
+          }
+          if (!ok) break;
+          if (leader) {
+            ptx::umma_commit(bar(bars->v_empty[t & 1]));
+            if (j + 1 < n) ptx::umma_commit(bar(bars->k_empty[(t + 1) & 1]));
+            else ptx::umma_commit(bar(bars->o_full));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        ++item;
+        w.next(a);
+      }
+      if (*abort_flag) {  // nothing may be in flight when tensor memory is freed
+        if (leader) ptx::umma_commit(bar(bars->drain));
+        __syncwarp();
+        const uint64_t t0 = ptx::globaltimer();
+        for (uint32_t i = 0; i != 0xFFFFFFFFu; ++i) {
+          if (ptx::mbar_try_wait(bar(bars->drain), 0)) break;
+          if ((i & 127u) == 0u && ptx::globaltimer() - t0 > kWaitNs) break;
+        }
+      }
+    }
+  } else if (warp < 8) {
+    ptx::regs_dec<88>();
+    // ---------------- expanders: thread = token of the tile ----------------
+    w.start(a, s_plan[0], s_plan[1], my_units);
+    const int r = tid - 128;
+    const int sw = r & 7;
+    const int64_t page_rows = static_cast<int64_t>(2 * cache.heads) << page_shift;
+    const int64_t to_values = static_cast<int64_t>(cache.heads) << page_shift;
+    constexpr int kVec = D / 32;  // 16-byte vectors of a row
+    // The row of this thread's token in the tile at `tok`, -1 if there is none.
+    auto find = [&](int tok) -> int64_t {
+      if (tok >= w.tile.hi) return -1;
+      const int id = __ldg(a.page_table + w.b * a.table_stride + (tok >> page_shift));
+      if (id < 0 || id >= cache.pages) return -1;
+      return id * page_rows + (static_cast<int64_t>(w.h) << page_shift) + (tok & (cache.page_size - 1));
+    };
+    struct Row {
+      uint4 v[kVec];
+      uint32_t s, z;
+    };
+    auto load = [&](int64_t row, Row& x) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        x.v[i] = row < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                         : __ldg(reinterpret_cast<const uint4*>(cache.packed + row * (D / 2)) + i);
+      x.s = row < 0 ? 0u : __ldg(cache.scales + row);
+      x.z = ASYM && row >= 0 ? __ldg(cache.zeros + row) : 0u;
+    };
+    auto store = [&](const Row& x, uint32_t at) {
+      const uint32_t z = ASYM ? x.z : 8u;
+      // -(1024 + z) and -(64 + z), exact.
+      const uint32_t b1 = (0xE400u + z) * 0x00010001u;
+      const uint32_t b16 = __half_as_ushort(__int2half_rn(-64 - static_cast<int>(z))) * 0x00010001u;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const uint32_t words[4] = {x.v[i].x, x.v[i].y, x.v[i].z, x.v[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = 4 * i + k;
+          ptx::sts128(at + (c >> 3) * L::kSub + r * 128 + (((c & 7) ^ sw) << 4), expand<ASYM>(words[k], b1, b16));
+        }
+      }
+    };
+    int t = 0;
+    bool ok = true;
+    while (ok && w.left > 0) {
+      const int n = w.steps();
+      const int base = w.tile.lo + w.s0 * kTok + r;
+      int64_t row = find(base);
+      int64_t row_next = n > 1 ? find(base + kTok) : -1;
+      Row kx, vx;
+      load(row, kx);
+      load(row < 0 ? row : row + to_values, vx);
+      for (int j = 0; j < n; ++j, ++t) {
+        const int64_t row_after = j + 2 < n ? find(base + (j + 2) * kTok) : -1;
+        const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+        const uint32_t finite = (vx.s & 0x7C00u) != 0x7C00u ? vx.s & 0x7FFFu : 0u;
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, finite);  // orders as the scales do
+        const float ks = f16_bits_to_float(kx.s), vs = f16_bits_to_float(vx.s);
+        // Keys.  The stage's last reader finished (first use: at once); the
+        // scales' entry was last used four tiles ago, by a softmax that has
+        // since handed on a later tile.
+        if (!(ok = wait_all(bar(bars->k_empty[t & 1]), ((t >> 1) & 1u) ^ 1u, wc))) break;
+        const int ring = t & (kScaleRing - 1);
+        s_scale[(ring * 2) * kTok + r] = ks + ks * 0.0f;  // an infinite scale gives NaN, as its values do
+        s_scale[(ring * 2 + 1) * kTok + r] = vs;
+        if (lane == 0) {
+          s_bits[ring * 8 + warp - 4] = live;
+          s_bits[ring * 8 + warp] = bits;
+        }
+        store(kx, ptx::smem_u32(smem + L::offK + (t & 1) * L::kTile));
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(bars->sc_full[ring]));
+          ptx::mbar_arrive(bar(bars->k_full[t & 1]));
+        }
+        if (j + 1 < n) load(row_next, kx);
+        if (!(ok = wait_all(bar(bars->v_empty[t & 1]), ((t >> 1) & 1u) ^ 1u, wc))) break;
+        store(vx, ptx::smem_u32(smem + L::offV + (t & 1) * L::kTile));
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(bars->v_full[t & 1]));
+        if (j + 1 < n) load(row_next < 0 ? row_next : row_next + to_values, vx);
+        row = row_next;
+        row_next = row_after;
+      }
+      if (!ok) break;
+      w.next(a);
+    }
+  } else {
+    ptx::regs_inc<192>();
+    // ---------------- softmax: thread = query row ----------------
+    w.start(a, s_plan[0], s_plan[1], my_units);
+    const int m = (warp - 8) >> 2;         // row tile
+    const int q4 = warp & 3;               // lanes of tensor memory this warp reads
+    const int r = m * 128 + q4 * 32 + lane;  // row of the item
+    const uint32_t lane_at = tmem + (static_cast<uint32_t>(32 * q4) << 16);
+    const uint32_t s_at = lane_at + m * kTok, o_at = lane_at + 2 * kTok + m * D;
+    const float sign = a.sm_scale > 0.0f ? 1.0f : (a.sm_scale < 0.0f ? -1.0f : 0.0f);
+    const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_token_stride % 8 == 0 && a.q_head_stride % 8 == 0;
+    int t = 0;
+    uint32_t item = 0;
+    bool ok = true;
+    while (ok && w.left > 0) {
+      const int n = w.steps();
+      const int r0 = w.rt * kRows;
+      const int rows = min(w.count * a.ratio - r0, kRows);
+      const bool live_row = r < rows;
+      const int i_tok = (r0 + (live_row ? r : 0)) / a.ratio;
+      const int hq = w.h * a.ratio + (r0 + (live_row ? r : 0)) - i_tok * a.ratio;
+      // ---- This row of Q.
+      float f;
+      int lo = 0, hi = 0;
+      {
+        uint32_t raw[D / 2];
+        const T* qp = static_cast<const T*>(a.q) + (w.first + i_tok) * a.q_token_stride + hq * a.q_head_stride;
+        if (q_vec) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(qp) + c);
+            raw[4 * c] = x.x; raw[4 * c + 1] = x.y; raw[4 * c + 2] = x.z; raw[4 * c + 3] = x.w;
+          }
+        } else {
+          const unsigned short* p = reinterpret_cast<const unsigned short*>(qp);
+#pragma unroll
+          for (int c = 0; c < D / 2; ++c)
+            raw[c] = __ldg(p + 2 * c) | (static_cast<uint32_t>(__ldg(p + 2 * c + 1)) << 16);
+        }
+        auto lo_of = [](uint32_t x) {
+          return std::is_same<T, __half>::value ? f16_bits_to_float(x & 0xFFFFu) : __uint_as_float(x << 16);
+        };
+        auto hi_of = [](uint32_t x) {
+          return std::is_same<T, __half>::value ? f16_bits_to_float(x >> 16) : __uint_as_float(x & 0xFFFF0000u);
+        };
+        float top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < D / 2; ++c) {
+          if (!live_row) raw[c] = 0u;
+          top = fmaxf(top, fmaxf(fabsf(lo_of(raw[c])), fabsf(hi_of(raw[c]))));
+        }
+        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        e = e < -100 ? -100 : e;
+        const float scale = sign * __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+        const uint32_t at = ptx::smem_u32(smem + L::offQ + m * L::kTile) + (r & 127) * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          // Elements 0 4, 1 5, 2 6, 3 7 of the block.
+          const uint32_t* x = raw + 4 * c;
+          const uint4 y = make_uint4(attn::pack_half2(lo_of(x[0]) * scale, lo_of(x[2]) * scale),
+                                     attn::pack_half2(hi_of(x[0]) * scale, hi_of(x[2]) * scale),
+                                     attn::pack_half2(lo_of(x[1]) * scale, lo_of(x[3]) * scale),
+                                     attn::pack_half2(hi_of(x[1]) * scale, hi_of(x[3]) * scale));
+          ptx::sts128(at + (c >> 3) * L::kSub + (((c & 7) ^ (r & 7)) << 4), y);
+        }
+        const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23) * (fabsf(a.sm_scale) * 1.4426950408889634f);
+        f = sign == 0.0f ? 1.0f : fminf(fmaxf(f1, 0x1p-126f), 0x1p127f);
+        if (live_row) a.visible(w.len - w.count + i_tok, w.len, lo, hi);
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::tc_fence_before();  // O of the item before has been read
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(bars->q_full));
+      // Tokens that all live rows of this warp see.
+      const int all_lo = __reduce_max_sync(0xffffffffu, live_row ? lo : 0);
+      const int all_hi = __reduce_min_sync(0xffffffffu, live_row ? hi : 0x7FFFFFFF);
+
+      float mx = kNegInf, nmf = 0.0f;
+      float2 l = make_float2(0.0f, 0.0f);
+      int x_run = 15;
+      const float2 f2 = make_float2(f, f);
+      for (int j = 0; j < n; ++j, ++t) {
+        const int ring = t & (kScaleRing - 1);
+        ok = wait_all(bar(bars->sc_full[ring]), (t / kScaleRing) & 1u, wc) &&
+             wait_all(bar(bars->s_full[m]), t & 1u, wc);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const float* const kc = s_scale + ring * 2 * kTok;
+        const float* const vc = kc + kTok;
+        float2 s[kTok / 2];
+        float top = kNegInf;
+        const int base = w.tile.lo + (w.s0 + j) * kTok;
+        const uint32_t live = s_bits[ring * 8] & s_bits[ring * 8 + 1] & s_bits[ring * 8 + 2] & s_bits[ring * 8 + 3];
+        const uint32_t bits = max(max(s_bits[ring * 8 + 4], s_bits[ring * 8 + 5]), max(s_bits[ring * 8 + 6], s_bits[ring * 8 + 7]));
+        const bool edge = base < all_lo || base + kTok > all_hi || live != 0xffffffffu;
+#pragma unroll
+        for (int c = 0; c < kTok; c += 32) {
+          uint32_t x[32];
+          ptx::tmem_ld_32x32b_x32(s_at + c, x);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(kc + c + i);
+            s[(c + i) / 2] = __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(k4.x, k4.y));
+            s[(c + i) / 2 + 1] = __fmul2_rn(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(k4.z, k4.w));
+          }
+        }
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < kTok; c += 32) {
+            const uint32_t here = s_bits[ring * 8 + c / 32];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const int tok = base + c + i;
+              if (((here >> i) & 1u) == 0u || tok < lo || tok >= hi) s[(c + i) / 2].x = kNegInf;
+              if (((here >> (i + 1)) & 1u) == 0u || tok + 1 < lo || tok + 1 >= hi) s[(c + i) / 2].y = kNegInf;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kTok / 2; ++i) top = fmaxf(top, fmaxf(s[i].x, s[i].y));
+        // ---- The reference of the weights, when it is too far behind.
+        const int x_new = min(x_run, 21 - static_cast<int>(bits >> 10));
+        const bool behind = top > mx && (mx == kNegInf || (top - mx) * f > kGrow);
+        if (__any_sync(0xffffffffu, behind) || x_new != x_run) {
+          const float m_new = fmaxf(mx, top);
+          float al = m_new == mx ? 1.0f : attn::ex2((mx - m_new) * f);
+          al *= __uint_as_float(static_cast<uint32_t>(127 + x_new - x_run) << 23);
+          mx = m_new;
+          x_run = x_new;
+          nmf = static_cast<float>(x_run) - (mx == kNegInf ? 0.0f : mx * f);
+          l = __fmul2_rn(l, make_float2(al, al));
+          if (j > 0) {  // the products of all earlier tiles are complete: S came after them
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+              uint32_t x[16];
+              ptx::tmem_ld_32x32b_x16(o_at + c, x);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * al);
+              tmem_st_32x32b_x16(o_at + c, x);
+            }
+          }
+        }
+        // ---- W = 2^x P s, over the columns of S.
+        const float2 nmf2 = make_float2(nmf, nmf);
+#pragma unroll
+        for (int c = 0; c < kTok; c += 32) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 v4 = *reinterpret_cast<const float4*>(vc + c + i);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float2 p = __ffma2_rn(s[(c + i) / 2 + k], f2, nmf2);
+              p.x = attn::ex2(p.x);
+              p.y = attn::ex2(p.y);
+              l = __fadd2_rn(l, p);
+              float2 y = __fmul2_rn(p, k == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
+              if (edge) {  // a hidden token's weight is 0 under any scale
+                y.x = p.x == 0.0f ? 0.0f : y.x;
+                y.y = p.y == 0.0f ? 0.0f : y.y;
+              }
+              pw[i / 2 + k] = attn::pack_half2(y.x, y.y);
+            }
+          }
+          tmem_st_32x32b_x16(s_at + c / 2, pw);
+        }
+        tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(bars->w_full[m]));
+      }
+      if (!ok) break;
+      // ---- O.
+      if (!(ok = wait_all(bar(bars->o_full), item & 1u, wc))) break;
+      ptx::tc_fence_after();
+      const bool whole = n == w.tile.steps;
+      const float sum = l.x + l.y;
+      const int at = (w.first + i_tok) * a.q_heads + hq;
+      const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (w.s0 == 0 ? 1 : 0)) * kRows + r;
+      const float back = __uint_as_float(static_cast<uint32_t>(127 - x_run) << 23);
+      const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : back;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t x[32];
+        ptx::tmem_ld_32x32b_x32(o_at + c, x);
+        ptx::tmem_ld_wait();
+        if (live_row) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            float v[8];  // columns 0 .. 7 of a block are its elements 0 4 1 5 2 6 3 7
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[(k >> 1) + 4 * (k & 1)] = __uint_as_float(x[i + k]) * inv;
+            if (whole) {
+              alignas(16) T y[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) store_as(y + k, v[k]);
+              *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + static_cast<int64_t>(at) * D + c + i) =
+                  *reinterpret_cast<const uint4*>(y);
+            } else {
+              float4* const dst = reinterpret_cast<float4*>(ws.o + slot * D + c + i);
+              dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+              dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+          }
+        }
+      }
+      if (live_row) {
+        const float top = mx * f;
+        if (!whole) {
+          ws.ml[slot * 2] = top;
+          ws.ml[slot * 2 + 1] = sum * back;
+        } else if (a.lse != nullptr) {
+          a.lse[at] = sum == 0.0f ? kNegInf
+                                  : (top + log2f(sum) - static_cast<float>(x_run)) * 0.6931471805599453f;
+        }
+      }
+      ++item;
+      w.next(a);
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int D, bool ASYM>
+cudaError_t launch_typed(const AttentionArgs& a, void* workspace, cudaStream_t stream) {
+  uint32_t* status = status_word();
+  if (status == nullptr) return cudaErrorInvalidSymbol;
+  const AttentionSpace ws = attention_space(workspace, a.batch, num_sms(), kRows, D);
+  auto kernel = attention_prefill_kernel<T, D, ASYM>;
+  constexpr int bytes = Smem<D>::kAlloc;
+  static_assert(bytes <= 227 * 1024, "one block's shared memory");
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  int shift = 0;
+  while ((1 << shift) < a.cache.page_size) ++shift;
+  kernel<<<ws.blocks, kThreadsP, bytes, stream>>>(a, ws, shift, status);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_attention_join<T>(a, ws, kRows, stream);
+}
+
+template <typename T>
+cudaError_t launch_any(const AttentionArgs& a, void* workspace, cudaStream_t stream) {
+  const bool asym = a.cache.zeros != nullptr;
+  if (a.cache.head_dim == 64)
+    return asym ? launch_typed<T, 64, true>(a, workspace, stream) : launch_typed<T, 64, false>(a, workspace, stream);
+  return asym ? launch_typed<T, 128, true>(a, workspace, stream) : launch_typed<T, 128, false>(a, workspace, stream);
+}
+
+}  // namespace
+
+int cache_prefill_row_tile() { return kRows; }
+
+cudaError_t launch_cache_prefill(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream) {
+  return t == DType::BF16 ? launch_any<__nv_bfloat16>(a, workspace, stream) : launch_any<__half>(a, workspace, stream);
+}
+
+}  // namespace int4lib

@@ -437,10 +437,11 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
   return e == cudaSuccess ? INT4_OK : int4lib::fail_cuda(e, "int4_cache_read");
 }
 
-// The sizes of an attention call, and the kernel that takes it.
+// The kernel that takes an attention call (*path becomes INT4_PATH_SIMT,
+// _DECODE or _PREFILL), and its workspace.
 static int attention_plan(const char* name, const int4lib::CacheView& view, DType t, int64_t rows,
                           int32_t q_heads, int32_t batch, int32_t max_pages, const void* out,
-                          int32_t path, bool* mma, size_t* bytes) {
+                          int32_t* path, size_t* bytes) {
   char msg[200];
   *bytes = 0;
   if (rows < 0 || q_heads < 1 || q_heads % view.heads != 0 || batch < 0 || max_pages < 0 ||
@@ -452,18 +453,26 @@ static int attention_plan(const char* name, const int4lib::CacheView& view, DTyp
                   name);
     return int4lib::fail(INT4_ERR_ARG, msg);
   }
-  *mma = int4lib::cache_attention_mma_supported(view, t, out, rows, batch, q_heads / view.heads, max_pages);
-  if (path == INT4_PATH_DECODE && !*mma) {
-    std::snprintf(msg, sizeof msg, "%s: the tensor-core kernels cannot run this call", name);
-    return int4lib::fail(INT4_ERR_UNSUPPORTED, msg);
-  }
-  if (path != INT4_PATH_AUTO && path != INT4_PATH_SIMT && path != INT4_PATH_DECODE) {
+  const int32_t asked = *path;
+  if (asked != INT4_PATH_AUTO && asked != INT4_PATH_SIMT && asked != INT4_PATH_DECODE && asked != INT4_PATH_PREFILL) {
     std::snprintf(msg, sizeof msg, "%s: unknown path", name);
     return int4lib::fail(INT4_ERR_ARG, msg);
   }
-  if (path == INT4_PATH_SIMT) *mma = false;
-  if (*mma && rows > 0 && batch > 0)
-    *bytes = int4lib::cache_attention_mma_workspace(view, rows, batch, q_heads / view.heads);
+  const int ratio = q_heads / view.heads;
+  const bool mma = int4lib::cache_attention_mma_supported(view, t, out, rows, batch, ratio, max_pages);
+  const bool prefill = int4lib::cache_prefill_supported(view, t, out, rows, batch, ratio, max_pages);
+  if ((asked == INT4_PATH_DECODE && !mma) || (asked == INT4_PATH_PREFILL && !prefill)) {
+    std::snprintf(msg, sizeof msg, "%s: the tensor-core kernel cannot run this call", name);
+    return int4lib::fail(INT4_ERR_UNSUPPORTED, msg);
+  }
+  if (asked == INT4_PATH_AUTO) {
+    *path = !mma ? INT4_PATH_SIMT : INT4_PATH_DECODE;
+    if (prefill && batch > 0 && rows * ratio >= int4lib::kPrefillRows * static_cast<int64_t>(batch))
+      *path = INT4_PATH_PREFILL;
+  }
+  if (rows == 0 || batch == 0) return INT4_OK;
+  if (*path == INT4_PATH_DECODE) *bytes = int4lib::cache_attention_mma_workspace(view, rows, batch, ratio);
+  if (*path == INT4_PATH_PREFILL) *bytes = int4lib::cache_prefill_workspace(view, batch);
   return INT4_OK;
 }
 
@@ -476,9 +485,8 @@ int int4_cache_attention_workspace_size(const int4_cache* cache, int32_t dtype, 
   int4lib::CacheView view;
   const int rc = cache_check(name, cache, dtype, &view);
   if (rc != INT4_OK) return rc;
-  bool mma;
   return attention_plan(name, view, static_cast<DType>(dtype), rows, q_heads, batch, max_pages, nullptr,
-                        path, &mma, bytes);
+                        &path, bytes);
 }
 
 int int4_cache_attention(const int4_cache* cache, const void* q, int64_t q_token_stride,
@@ -492,9 +500,8 @@ int int4_cache_attention(const int4_cache* cache, const void* q, int64_t q_token
   const int rc = cache_check(name, cache, dtype, &view);
   if (rc != INT4_OK) return rc;
   const DType t = static_cast<DType>(dtype);
-  bool mma;
   size_t need;
-  const int rp = attention_plan(name, view, t, rows, q_heads, batch, max_pages, out, path, &mma, &need);
+  const int rp = attention_plan(name, view, t, rows, q_heads, batch, max_pages, out, &path, &need);
   if (rp != INT4_OK) return rp;
   if (window < 0 || !std::isfinite(sm_scale))
     return int4lib::fail(INT4_ERR_ARG, "int4_cache_attention: need window >= 0 and a finite sm_scale");
@@ -523,8 +530,9 @@ int int4_cache_attention(const int4_cache* cache, const void* q, int64_t q_token
                                     table_stride, kv_lens, q_starts, static_cast<int32_t>(rows), batch, max_pages, q_heads,
                                     q_heads / view.heads, causal != 0 ? 1 : 0, window, sm_scale};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = mma ? int4lib::launch_cache_attention_mma(a, t, workspace, s)
-                            : int4lib::launch_cache_attention_any(a, t, s);
+  const cudaError_t e = path == INT4_PATH_SIMT     ? int4lib::launch_cache_attention_any(a, t, s)
+                        : path == INT4_PATH_DECODE ? int4lib::launch_cache_attention_mma(a, t, workspace, s)
+                                                   : int4lib::launch_cache_prefill(a, t, workspace, s);
   return e == cudaSuccess ? INT4_OK : int4lib::fail_cuda(e, name);
 }
 

@@ -100,6 +100,16 @@ bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out,
                                    int ratio, int64_t max_pages);
 size_t cache_attention_mma_workspace(const CacheView& c, int64_t rows, int64_t batch, int ratio);
 cudaError_t launch_cache_attention_mma(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
+// cache_prefill.cu: the tcgen05 kernel for many query rows, its workspace
+// likewise.
+int cache_prefill_row_tile();
+// Query rows of one head (tokens times ratio) of an average sequence from which
+// it is taken.
+constexpr int kPrefillRows = 64;
+bool cache_prefill_supported(const CacheView& c, DType t, const void* out, int64_t rows, int64_t batch, int ratio,
+                             int64_t max_pages);
+size_t cache_prefill_workspace(const CacheView& c, int64_t batch);
+cudaError_t launch_cache_prefill(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
 // cache_attention_<D>.cu: the kernels for heads of D elements; rt: query rows
 // of a tile.
 cudaError_t launch_cache_attention_64(const AttentionArgs& a, DType t, int rt, void* workspace, cudaStream_t stream);

@@ -339,7 +339,8 @@ int int4_matmul_select(int32_t x_dtype, int64_t K, int32_t group, int64_t M, int
  *   scales [pages, 2, heads, page_size, G] fp16 bits, G = ceil(head_dim / group)
  *   zeros  [pages, 2, heads, page_size, G] uint8, or NULL: the symmetric scheme
  *
- * dense, keys at index 0 and values at index 1 of the second dimension.  Token
+ * dense, keys at index 0 and values at index 1 of the second dimension; the
+ * scales are not negative (int4_cache_write's never are).  Token
  * `slot` lies in page slot / page_size at offset slot % page_size.  Its row of
  * one head is coded bit for bit as int4_quantize codes a row of K = head_dim
  * weights (zeros == NULL), or int4_quantize_affine (zeros given).
@@ -426,15 +427,19 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * Accuracy: S, the softmax's maximum and sum, and out's sums are fp32.  For
  * fp32 q so are the products.  For bf16 and fp16 q the products run on tensor
  * cores: q and the codes exactly (elements of q below 2^-24 of the row's
- * largest to 2^-38 of it), the weights exp(S_j) s_j rounded to fp16, 2^-11
- * relative each.  Deterministic for given sizes, lengths and device.
+ * largest to 2^-38 of it), the weights exp(S_j - max) s_j, s_j the value
+ * scales, in fp16: off by at most 2^-11 of themselves, or, where they are more
+ * than 2^20 below the largest, 2^-32 of that.  Deterministic for given sizes,
+ * lengths and device.
  * NaN or infinity in a query makes its own rows NaN.
  *
- * `path`: INT4_PATH_AUTO takes the tensor-core kernels (INT4_PATH_DECODE)
- * where they can run: bf16 or fp16 q, head_dim 64, 96, 128 or 256 in groups of
- * 32, 64, 128 or head_dim (96: 32 or 96), page_size a power of two from 16 on,
- * max_pages * page_size <= 2^30, packed, scales and zeros 16-byte and out
- * 8-byte aligned; else the general kernel (INT4_PATH_SIMT).  A forced path that
+ * `path`: INT4_PATH_AUTO takes a tensor-core kernel where one can run, else the
+ * general kernel (INT4_PATH_SIMT).  INT4_PATH_DECODE, for few query rows: bf16 or
+ * fp16 q, head_dim 64, 96, 128 or 256 in groups of 32, 64, 128 or head_dim (96:
+ * 32 or 96), page_size a power of two from 16 on, max_pages * page_size <= 2^30
+ * (and steps of 128 tokens over all heads below 2^30), packed, scales and zeros
+ * 16-byte and out 8-byte aligned.  INT4_PATH_PREFILL, for many: of those,
+ * head_dim 64 or 128 in one group, out 16-byte aligned.  A forced path that
  * cannot run the call returns INT4_ERR_UNSUPPORTED.
  *
  * workspace: at least int4_cache_attention_workspace_size bytes (else

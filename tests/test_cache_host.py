@@ -72,7 +72,7 @@ def test_cache_attention_rejects_bad_arguments(L):
     assert call(t=4) == q4.ERR_DTYPE
     for bad in (dict(rows=-1), dict(hq=3), dict(hq=0), dict(batch=-1), dict(pages=-1), dict(window=-1),
                 dict(scale=math.nan), dict(scale=math.inf), dict(rows=7), dict(q=None), dict(table=None),
-                dict(lens=None), dict(out=None), dict(path=9), dict(path=q4.PATH_PREFILL), dict(n=64),
+                dict(lens=None), dict(out=None), dict(path=9), dict(path=-1), dict(n=64),
                 dict(rows=1 << 40), dict(c=cache(head_dim=0))):
         assert call(**bad) == q4.ERR_ARG, bad
     for bad in (dict(q=257), dict(out=257), dict(table=258), dict(lens=258), dict(starts=258), dict(lse=258),

@@ -180,6 +180,20 @@ def test_attention(D, group, dtype, path, affine, ratio, counts):
     run_attention(2, ratio, D, group, 16, [37, 1, 300, 129, 64], counts, DTYPES[dtype], affine=affine, path=path)
 
 
+@pytest.mark.parametrize("affine", [False, True])
+@pytest.mark.parametrize("D, dtype", [(64, "bf16"), (64, "f16"), (128, "bf16"), (128, "f16")])
+@pytest.mark.parametrize("H, ratio, lens, counts", [
+    (1, 1, [128], [128]),                       # one tile of keys, one of rows
+    (1, 1, [1], [1]),
+    (2, 4, [500, 37, 300], [100, 37, 1]),
+    (1, 8, [1500, 129], [200, 70]),             # several row tiles
+    (3, 3, [1000], [333]),                      # a ratio that does not divide the tile
+    (2, 1, [3000, 5], [600, 9]),                # a sequence of fewer tokens than queries
+])
+def test_attention_many_rows(D, dtype, affine, H, ratio, lens, counts):
+    run_attention(H, ratio, D, D, 32, lens, counts, DTYPES[dtype], affine=affine, path=q4.PATH_PREFILL)
+
+
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 63, 65, 127, 128, 129, 255, 257, 1000, 4097])
 def test_attention_lengths(n):
     run_attention(1, 8, 64, 64, 64, [n], [1], torch.bfloat16, seed=n)
@@ -192,7 +206,7 @@ def test_attention_page_sizes(page_size):
     run_attention(2, 4, 64, 32, page_size, [333, 40, 7], [1, 1, 1], torch.bfloat16, seed=page_size)
 
 
-@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE])
+@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE, q4.PATH_PREFILL])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("window", [None, 1, 2, 31, 100, 5000])
 def test_attention_masks(path, causal, window):
@@ -245,7 +259,7 @@ def attention_setup(H=2, ratio=4, D=128, group=128, S=16, lens=(70, 33), seed=1,
     return q, packed, scales, zeros, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), group
 
 
-@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE])
+@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE, q4.PATH_PREFILL])
 def test_attention_hidden_places_do_not_count(path):
     """NaN and infinite scales past the sequences' ends, in pages of nobody,
     and before a window change nothing, bit for bit."""
@@ -270,7 +284,7 @@ def test_attention_hidden_places_do_not_count(path):
             assert torch.equal(a, b) and torch.equal(a, c)
 
 
-@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE])
+@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE, q4.PATH_PREFILL])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 def test_attention_tokens_hidden_from_some_rows(path, bad):
     """A value scale that is not finite reaches only the rows that see its
@@ -288,7 +302,7 @@ def test_attention_tokens_hidden_from_some_rows(path, bad):
         assert_attention_close((out[keep], lse[keep]), tuple(x[keep] for x in want))
 
 
-@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE])
+@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE, q4.PATH_PREFILL])
 def test_attention_unknown_pages_hold_no_tokens(path):
     q, packed, scales, zeros, table, lens, group = attention_setup(lens=(200, 33, 64))
     table[0, 2], table[0, 5], table[2, :] = -7, packed.shape[0], 1 << 30
@@ -297,7 +311,7 @@ def test_attention_unknown_pages_hold_no_tokens(path):
     assert (got[0][2] == 0).all() and torch.isinf(got[1][2]).all()
 
 
-@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE])
+@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE, q4.PATH_PREFILL])
 def test_attention_lengths_outside_the_table(path):
     """A negative length counts as 0, one past the table as what the table holds."""
     q, packed, scales, zeros, table, lens, group = attention_setup(extra=0, lens=(80, 33))
@@ -306,7 +320,7 @@ def test_attention_lengths_outside_the_table(path):
     assert_attention_close(got, attention_ref(q, packed, scales, zeros, table, [80, 0], [1, 1], group))
 
 
-@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE])
+@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE, q4.PATH_PREFILL])
 def test_attention_rows_of_no_sequence_stay(path):
     q, packed, scales, zeros, table, lens, group = attention_setup()
     q = q.repeat(4, 1, 1)
@@ -335,7 +349,7 @@ def test_attention_strided_and_unaligned_queries():
                                                    zeros=zeros), want)
 
 
-@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE])
+@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE, q4.PATH_PREFILL])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 def test_attention_nan_in_a_query_stays_in_its_rows(path, bad):
     q, packed, scales, zeros, table, lens, group = attention_setup()
