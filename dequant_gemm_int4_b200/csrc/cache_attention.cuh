@@ -1005,6 +1005,128 @@ __global__ void __launch_bounds__(256)
     a.lse[at] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
+// The join for large row tiles, where an item's pieces are few and its rows
+// many: block (c, i) joins rows [8 i, 8 i + 8) of the item that begins in share
+// c and goes on in the next ones, if there is one; blocks (ws.blocks + b, i)
+// write the rows of sequence b's tiles that see nothing.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    attention_join_items_kernel(const __grid_constant__ AttentionArgs a, const AttentionSpace ws, const int RT) {
+  constexpr float kNegInf = -__builtin_huge_valf();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int D = a.cache.head_dim;
+  const int rr = blockIdx.y * 8 + warp;  // row of the tile
+  auto store = [&](int at, int d, float4 v) {
+    alignas(8) T four[4];
+    store_as(four, v.x);
+    store_as(four + 1, v.y);
+    store_as(four + 2, v.z);
+    store_as(four + 3, v.w);
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + static_cast<int64_t>(at) * D + d) =
+        *reinterpret_cast<const uint2*>(four);
+  };
+  if (static_cast<int>(blockIdx.x) >= ws.blocks) {
+    const int b = blockIdx.x - ws.blocks;
+    int first, count;
+    a.queries(b, first, count);
+    const int len = a.kv_len(b), n = row_tiles(a, count, RT);
+    ptx::grid_dependency_wait();
+    for (int rt = 0; rt < n; ++rt) {
+      RowTile tile;
+      tile.set(a, len, count, rt, RT);
+      const int r = rt * RT + rr;
+      if (tile.steps > 0 || r >= count * a.ratio) continue;
+      const int i = r / a.ratio;
+      for (int h = 0; h < a.cache.heads; ++h) {
+        const int at = (first + i) * a.q_heads + h * a.ratio + r - i * a.ratio;
+        for (int d = lane * 4; d < D; d += 128) store(at, d, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        if (lane == 0 && a.lse != nullptr) a.lse[at] = kNegInf;
+      }
+    }
+    return;
+  }
+  ptx::grid_dependency_wait();
+  const Shares shares(ws.prefix[a.batch], ws.blocks);
+  const int c = blockIdx.x;
+  if (c + 1 >= shares.active) return;
+  const int begin = shares.begin(c), last = shares.begin(c + 1) - 1;
+  int b = 0, hi_b = a.batch;  // the sequence of unit `last`
+  while (hi_b - b > 1) {
+    const int mid = (b + hi_b) >> 1;
+    if (ws.prefix[mid] <= last) b = mid; else hi_b = mid;
+  }
+  int first, count;
+  a.queries(b, first, count);
+  const int len = a.kv_len(b), n = row_tiles(a, count, RT);
+  // Its head and row tile, a lane to each of 32 tiles at a time.
+  int per_head = 0;
+  for (int i = lane; i < n; i += 32) {
+    RowTile tile;
+    tile.set(a, len, count, i, RT);
+    per_head += tile.steps;
+  }
+  per_head = __reduce_add_sync(0xffffffffu, per_head);
+  const int in_seq = last - ws.prefix[b];
+  const int h = in_seq / per_head, off = in_seq - h * per_head;
+  int rt = 0, before = 0, steps = 0;
+  for (int i0 = 0, sum = 0; i0 < n; i0 += 32) {
+    RowTile tile;
+    tile.steps = 0;
+    if (i0 + lane < n) tile.set(a, len, count, i0 + lane, RT);
+    int upto = tile.steps;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, sum + upto > off);
+    if (past != 0u) {
+      const int at = __ffs(past) - 1;
+      rt = i0 + at;
+      steps = __shfl_sync(0xffffffffu, tile.steps, at);
+      before = sum + __shfl_sync(0xffffffffu, upto, at) - steps;
+      break;
+    }
+    sum += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  const int item = ws.prefix[b] + h * per_head + before;
+  if (item < begin || item + steps <= last + 1) return;  // begun earlier, or ends here
+  const int p_end = shares.block_of(item + steps - 1) + 1;
+  const int r = rt * RT + rr;
+  if (r >= count * a.ratio) return;
+  auto slot = [&](int p) { return static_cast<int64_t>(2 * p + (p == c ? 1 : 0)) * RT + rr; };
+  float top = kNegInf, sum = 0.0f;
+  for (int p = c; p < p_end; ++p) top = fmaxf(top, ws.ml[slot(p) * 2]);
+  float4 v[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  for (int p = c; p < p_end; ++p) {
+    const int64_t s = slot(p);
+    const float mp = ws.ml[s * 2];
+    const float w = mp == top ? 1.0f : attn::ex2(mp - top);
+    sum = fmaf(w, ws.ml[s * 2 + 1], sum);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int d = i * 128 + lane * 4;
+      if (d < D) {
+        const float4 x = *reinterpret_cast<const float4*>(ws.o + s * D + d);
+        v[i].x = fmaf(w, x.x, v[i].x);
+        v[i].y = fmaf(w, x.y, v[i].y);
+        v[i].z = fmaf(w, x.z, v[i].z);
+        v[i].w = fmaf(w, x.w, v[i].w);
+      }
+    }
+  }
+  const int i = r / a.ratio;
+  const int at = (first + i) * a.q_heads + h * a.ratio + r - i * a.ratio;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int d = k * 128 + lane * 4;
+    if (d < D) store(at, d, make_float4(v[k].x * inv, v[k].y * inv, v[k].z * inv, v[k].w * inv));
+  }
+  if (lane == 0 && a.lse != nullptr)
+    a.lse[at] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
 // ---- Host side ------------------------------------------------------------
 
 // Query rows of a tile: the smallest of 8, 16 and 32 that holds the rows of an
@@ -1030,14 +1152,12 @@ inline size_t attention_space_bytes(int64_t batch, int64_t blocks, int rt, int h
   return attention_prefix_bytes(batch) + (2 * blocks * rt * (head_dim + 2) * sizeof(float) + 255) / 256 * 256;
 }
 
-// The join, launched early where the kernel before it lets it (it waits for
-// that kernel's end before it reads).
-template <typename T>
-cudaError_t launch_attention_join(const AttentionArgs& a, const AttentionSpace& ws, int rt, cudaStream_t stream) {
-  const int rows = a.rows * a.q_heads;
-  const int wpr = rows <= 2048 ? 8 : 1;
+// The joins, launched early where the kernel before lets them (they wait for
+// its end before they read).
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(wpr == 8 ? rows : (rows + 7) / 8));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1045,7 +1165,17 @@ cudaError_t launch_attention_join(const AttentionArgs& a, const AttentionSpace& 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T>, a, ws, rt, wpr);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename T>
+cudaError_t launch_attention_join(const AttentionArgs& a, const AttentionSpace& ws, int rt, cudaStream_t stream) {
+  const int rows = a.rows * a.q_heads;
+  const int wpr = rows <= 2048 ? 8 : 1;
+  return launch_dependent(attention_join_kernel<T>, dim3(wpr == 8 ? rows : (rows + 7) / 8), stream, a, ws, rt, wpr);
+}
+template <typename T>
+cudaError_t launch_attention_join_items(const AttentionArgs& a, const AttentionSpace& ws, int rt, cudaStream_t stream) {
+  return launch_dependent(attention_join_items_kernel<T>, dim3(ws.blocks + a.batch, rt / 8), stream, a, ws, rt);
 }
 
 template <class C>

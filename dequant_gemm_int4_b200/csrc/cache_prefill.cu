@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   uint32_t* const misc = reinterpret_cast<uint32_t*>(smem + L::offMisc);  // TMEM address, abort flag, plan
   volatile uint32_t* const abort_flag = misc + 1;
   int* const s_plan = reinterpret_cast<int*>(misc + 2);  // sequence, offset; then scan[4]
+  volatile int* const s_steps = reinterpret_cast<volatile int*>(misc + 8);  // [2]: tiles of an item, 0 after the last
   float* const s_scale = reinterpret_cast<float*>(smem + L::offScale);
   volatile uint32_t* const s_bits = reinterpret_cast<volatile uint32_t*>(smem + L::offBits);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -313,7 +314,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     ptx::regs_dec<40>();
     if (warp == 0) {
       // ---------------- MMA issuer ----------------
-      w.start(a, s_plan[0], s_plan[1], my_units);
       const bool leader = ptx::elect_one();
       constexpr uint32_t id_s = instr_desc(kTok, false), id_o = instr_desc(D, true);
       const uint32_t q_at = ptx::smem_u32(smem + L::offQ), k_at = ptx::smem_u32(smem + L::offK),
@@ -343,10 +343,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       int t = 0;  // tiles before this one
       uint32_t item = 0;
       bool ok = true;
-      while (ok && w.left > 0) {
-        const int n = w.steps();
-        ok = wait_all(bar(bars->q_full), item & 1u, wc) && wait_all(bar(bars->k_full[t & 1]), (t >> 1) & 1u, wc);
-        if (!ok) break;
+      while (true) {
+        if (!(ok = wait_all(bar(bars->q_full), item & 1u, wc))) break;
+        const int n = s_steps[item & 1u];
+        if (n == 0) break;
+        if (!(ok = wait_all(bar(bars->k_full[t & 1]), (t >> 1) & 1u, wc))) break;
         ptx::tc_fence_after();
         s_mma(0, t & 1);
         s_mma(1, t & 1);
@@ -379,7 +380,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         }
         if (!ok) break;
         ++item;
-        w.next(a);
       }
       if (*abort_flag) {  // nothing may be in flight when tensor memory is freed
         if (leader) ptx::umma_commit(bar(bars->drain));
@@ -552,6 +552,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       }
       ptx::fence_proxy_async_smem();
       ptx::tc_fence_before();  // O of the item before has been read
+      if (warp == 8) s_steps[item & 1u] = n;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(bars->q_full));
       // Tokens that all live rows of this warp see.
@@ -570,38 +571,44 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         ptx::tc_fence_after();
         const float* const kc = s_scale + ring * 2 * kTok;
         const float* const vc = kc + kTok;
-        float2 s[kTok / 2];
-        float top = kNegInf;
         const int base = w.tile.lo + (w.s0 + j) * kTok;
         const uint32_t live = s_bits[ring * 8] & s_bits[ring * 8 + 1] & s_bits[ring * 8 + 2] & s_bits[ring * 8 + 3];
         const uint32_t bits = max(max(s_bits[ring * 8 + 4], s_bits[ring * 8 + 5]), max(s_bits[ring * 8 + 6], s_bits[ring * 8 + 7]));
         const bool edge = base < all_lo || base + kTok > all_hi || live != 0xffffffffu;
-#pragma unroll
-        for (int c = 0; c < kTok; c += 32) {
-          uint32_t x[32];
-          ptx::tmem_ld_32x32b_x32(s_at + c, x);
-          ptx::tmem_ld_wait();
+        // S / f of 32 columns from x: times the key scales, hidden tokens -inf.
+        auto scores = [&](int c, const uint32_t (&x)[32], float2 (&s)[16]) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             const float4 k4 = *reinterpret_cast<const float4*>(kc + c + i);
-            s[(c + i) / 2] = __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(k4.x, k4.y));
-            s[(c + i) / 2 + 1] = __fmul2_rn(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(k4.z, k4.w));
+            s[i / 2] = __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(k4.x, k4.y));
+            s[i / 2 + 1] = __fmul2_rn(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(k4.z, k4.w));
           }
-        }
-        if (edge) {
-#pragma unroll
-          for (int c = 0; c < kTok; c += 32) {
+          if (edge) {
             const uint32_t here = s_bits[ring * 8 + c / 32];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const int tok = base + c + i;
-              if (((here >> i) & 1u) == 0u || tok < lo || tok >= hi) s[(c + i) / 2].x = kNegInf;
-              if (((here >> (i + 1)) & 1u) == 0u || tok + 1 < lo || tok + 1 >= hi) s[(c + i) / 2].y = kNegInf;
+              if (((here >> i) & 1u) == 0u || tok < lo || tok >= hi) s[i / 2].x = kNegInf;
+              if (((here >> (i + 1)) & 1u) == 0u || tok + 1 < lo || tok + 1 >= hi) s[i / 2].y = kNegInf;
             }
           }
-        }
+        };
+        // ---- The row's maximum over the tile.  S is read twice, 32 columns
+        // at a time with the next 32 on their way, and not kept in between.
+        float top = kNegInf;
+        {
+          uint32_t x[2][32];
+          ptx::tmem_ld_32x32b_x32(s_at, x[0]);
 #pragma unroll
-        for (int i = 0; i < kTok / 2; ++i) top = fmaxf(top, fmaxf(s[i].x, s[i].y));
+          for (int c = 0; c < kTok; c += 32) {
+            ptx::tmem_ld_wait();
+            if (c + 32 < kTok) ptx::tmem_ld_32x32b_x32(s_at + c + 32, x[(c / 32 + 1) & 1]);
+            float2 s[16];
+            scores(c, x[(c / 32) & 1], s);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(s[i].x, s[i].y));
+          }
+        }
         // ---- The reference of the weights, when it is too far behind.
         const int x_new = min(x_run, 21 - static_cast<int>(bits >> 10));
         const bool behind = top > mx && (mx == kNegInf || (top - mx) * f > kGrow);
@@ -627,27 +634,35 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         }
         // ---- W = 2^x P s, over the columns of S.
         const float2 nmf2 = make_float2(nmf, nmf);
+        {
+          uint32_t x[2][32];
+          ptx::tmem_ld_32x32b_x32(s_at, x[0]);
 #pragma unroll
-        for (int c = 0; c < kTok; c += 32) {
-          uint32_t pw[16];
+          for (int c = 0; c < kTok; c += 32) {
+            ptx::tmem_ld_wait();
+            if (c + 32 < kTok) ptx::tmem_ld_32x32b_x32(s_at + c + 32, x[(c / 32 + 1) & 1]);
+            float2 s[16];
+            scores(c, x[(c / 32) & 1], s);
+            uint32_t pw[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 v4 = *reinterpret_cast<const float4*>(vc + c + i);
+            for (int i = 0; i < 32; i += 4) {
+              const float4 v4 = *reinterpret_cast<const float4*>(vc + c + i);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float2 p = __ffma2_rn(s[(c + i) / 2 + k], f2, nmf2);
-              p.x = attn::ex2(p.x);
-              p.y = attn::ex2(p.y);
-              l = __fadd2_rn(l, p);
-              float2 y = __fmul2_rn(p, k == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
-              if (edge) {  // a hidden token's weight is 0 under any scale
-                y.x = p.x == 0.0f ? 0.0f : y.x;
-                y.y = p.y == 0.0f ? 0.0f : y.y;
+              for (int k = 0; k < 2; ++k) {
+                float2 p = __ffma2_rn(s[i / 2 + k], f2, nmf2);
+                p.x = attn::ex2(p.x);
+                p.y = attn::ex2(p.y);
+                l = __fadd2_rn(l, p);
+                float2 y = __fmul2_rn(p, k == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
+                if (edge) {  // a hidden token's weight is 0 under any scale
+                  y.x = p.x == 0.0f ? 0.0f : y.x;
+                  y.y = p.y == 0.0f ? 0.0f : y.y;
+                }
+                pw[i / 2 + k] = attn::pack_half2(y.x, y.y);
               }
-              pw[i / 2 + k] = attn::pack_half2(y.x, y.y);
             }
+            tmem_st_32x32b_x16(s_at + c / 2, pw);  // over columns that have been read
           }
-          tmem_st_32x32b_x16(s_at + c / 2, pw);
         }
         tmem_st_wait();
         ptx::tc_fence_before();
@@ -702,6 +717,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       ++item;
       w.next(a);
     }
+    if (ok) {  // no more items
+      if (warp == 8) s_steps[item & 1u] = 0;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(bars->q_full));
+    }
   }
 
   ptx::tc_fence_before();
@@ -727,7 +747,7 @@ cudaError_t launch_typed(const AttentionArgs& a, void* workspace, cudaStream_t s
   kernel<<<ws.blocks, kThreadsP, bytes, stream>>>(a, ws, shift, status);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_attention_join<T>(a, ws, kRows, stream);
+  return launch_attention_join_items<T>(a, ws, kRows, stream);
 }
 
 template <typename T>
