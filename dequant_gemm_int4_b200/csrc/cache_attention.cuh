@@ -793,7 +793,6 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-#pragma unroll
         float sum = j == 0 ? l[nt].x : l[nt].y;
 #pragma unroll
         for (int o2 = 4; o2 < 32; o2 <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);

@@ -8,7 +8,7 @@
 //   S_m = Q_m K^T         128 x 128 x D, both operands in shared memory
 //   O_m += W_m V          128 x D x 128, W from tensor memory
 // Tensor memory holds S_0, S_1 (fp32, 128 columns each; W_m, fp16, overlays the
-// first half of S_m once S_m has been read) and O_0, O_1 (D columns each).
+// the first half of S_m once S_m has been read) and O_0, O_1 (D columns each).
 //
 // Roles of the block's 16 warps:
 //   warps 0-3    warp 0 issues the MMAs; the others only lend their registers
@@ -23,8 +23,11 @@
 // key scale multiplies its column of S in fp32, its value scale the weight,
 // W = 2^x P s rounded to fp16 once (x: a power of two that keeps it in range).
 // So one group a head is required here (group = head_dim).  S, the maximum and
-// the sum are fp32; O is fp32 in tensor memory, rescaled only when a row's
-// maximum has grown by more than 2^8 (weights may reach 2^8 until then).
+// the sum are fp32; O is fp32 in tensor memory.  Weights are taken relative to a
+// reference that follows the row's maximum only when that has passed it by
+// more than a factor 2^8: a tile's weights are computed at once under the old
+// reference, and again, after O has been rescaled, in the rare tile that
+// turns out to need a new one.
 //
 // Inside blocks of 8 elements, keys and queries are stored in the order 0, 4,
 // 1, 5, 2, 6, 3, 7 in which a code word expands pair by pair; O's columns come
@@ -63,8 +66,8 @@ struct Smem {
   static constexpr int offK = offQ + 2 * kTile;  // two stages
   static constexpr int offV = offK + 2 * kTile;  // two stages
   static constexpr int offScale = offV + 2 * kTile;             // [ring][key, value][128] fp32
-  static constexpr int offBits = offScale + kScaleRing * 2 * kTok * 4;  // [ring][4 + 4]: live tokens, largest value scales
-  static constexpr int offBar = offBits + kScaleRing * 8 * 4;
+  static constexpr int offBits = offScale + kScaleRing * 2 * kTok * 4;  // [ring][3][4]: see Bits
+  static constexpr int offBar = offBits + kScaleRing * 12 * 4;
   static constexpr int offMisc = offBar + static_cast<int>(sizeof(Bars));
   static constexpr int kAlloc = offMisc + 64 + 1024;  // slack to align the base to 1024
 };
@@ -100,12 +103,25 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // fp16 operands, fp32 result, M = 128; n_major: B contiguous along N.
 __device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool n_major) {
   return (1u << 4) | (n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
+
+// What the expanders say of a tile besides its scales: word i is that of tokens
+// [32 i, 32 i + 32).
+struct Bits {
+  uint32_t live[4];  // tokens that are there
+  uint32_t bad[4];   // of those, the ones whose value scale is not finite
+  uint32_t top[4];   // the largest finite value scale, as fp16 bits
+};
 
 struct Wait {
   volatile uint32_t* abort;
@@ -168,7 +184,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   int* const s_plan = reinterpret_cast<int*>(misc + 2);  // sequence, offset; then scan[4]
   volatile int* const s_steps = reinterpret_cast<volatile int*>(misc + 8);  // [2]: tiles of an item, 0 after the last
   float* const s_scale = reinterpret_cast<float*>(smem + L::offScale);
-  volatile uint32_t* const s_bits = reinterpret_cast<volatile uint32_t*>(smem + L::offBits);
+  Bits* const s_bits = reinterpret_cast<Bits*>(smem + L::offBits);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [&](uint64_t& b) { return ptx::smem_u32(&b); };
   const Wait wc{abort_flag, status};
@@ -305,7 +321,22 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       } while (tile.steps == 0);
     }
   };
-  Walk w;
+  // Each warp of a role keeps its place in shared memory (all its lanes agree).
+  __shared__ Walk s_walk[16];
+  Walk& w = s_walk[warp];
+  auto walk_start = [&]() {
+    Walk x;
+    x.start(a, s_plan[0], s_plan[1], my_units);
+    if (lane == 0) w = x;
+    __syncwarp();
+  };
+  auto walk_next = [&]() {
+    Walk x = w;
+    x.next(a);
+    __syncwarp();
+    if (lane == 0) w = x;
+    __syncwarp();
+  };
 
   // Registers a thread: 40 for the MMA warps, 88 for the expanders, 192 for
   // the softmax; 128 * 40 + 128 * 88 + 256 * 192 = 65536 = 512 * 128, what the
@@ -394,7 +425,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   } else if (warp < 8) {
     ptx::regs_dec<88>();
     // ---------------- expanders: thread = token of the tile ----------------
-    w.start(a, s_plan[0], s_plan[1], my_units);
+    walk_start();
     const int r = tid - 128;
     const int sw = r & 7;
     const int64_t page_rows = static_cast<int64_t>(2 * cache.heads) << page_shift;
@@ -446,10 +477,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       load(row < 0 ? row : row + to_values, vx);
       for (int j = 0; j < n; ++j, ++t) {
         const int64_t row_after = j + 2 < n ? find(base + (j + 2) * kTok) : -1;
+        const bool finite = (vx.s & 0x7C00u) != 0x7C00u;
         const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
-        const uint32_t finite = (vx.s & 0x7C00u) != 0x7C00u ? vx.s & 0x7FFFu : 0u;
-        const uint32_t bits = __reduce_max_sync(0xffffffffu, finite);  // orders as the scales do
-        const float ks = f16_bits_to_float(kx.s), vs = f16_bits_to_float(vx.s);
+        const uint32_t bad = __ballot_sync(0xffffffffu, !finite);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, finite ? vx.s & 0x7FFFu : 0u);  // orders as the scales do
+        const float ks = f16_bits_to_float(kx.s), vs = finite ? f16_bits_to_float(vx.s) : 0.0f;
         // Keys.  The stage's last reader finished (first use: at once); the
         // scales' entry was last used four tiles ago, by a softmax that has
         // since handed on a later tile.
@@ -458,8 +490,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         s_scale[(ring * 2) * kTok + r] = ks + ks * 0.0f;  // an infinite scale gives NaN, as its values do
         s_scale[(ring * 2 + 1) * kTok + r] = vs;
         if (lane == 0) {
-          s_bits[ring * 8 + warp - 4] = live;
-          s_bits[ring * 8 + warp] = bits;
+          s_bits[ring].live[warp - 4] = live;
+          s_bits[ring].bad[warp - 4] = bad;
+          s_bits[ring].top[warp - 4] = top;
         }
         store(kx, ptx::smem_u32(smem + L::offK + (t & 1) * L::kTile));
         ptx::fence_proxy_async_smem();
@@ -479,15 +512,15 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         row_next = row_after;
       }
       if (!ok) break;
-      w.next(a);
+      walk_next();
     }
   } else {
     ptx::regs_inc<192>();
     // ---------------- softmax: thread = query row ----------------
-    w.start(a, s_plan[0], s_plan[1], my_units);
-    const int m = (warp - 8) >> 2;         // row tile
-    const int q4 = warp & 3;               // lanes of tensor memory this warp reads
-    const int r = m * 128 + q4 * 32 + lane;  // row of the item
+    walk_start();
+    const int m = (warp - 8) >> 2;           // row tile
+    const int q4 = warp & 3;                 // lanes of tensor memory this warp reads
+    const int in_tile = q4 * 32 + lane, r = m * 128 + in_tile;  // row of the item
     const uint32_t lane_at = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     const uint32_t s_at = lane_at + m * kTok, o_at = lane_at + 2 * kTok + m * D;
     const float sign = a.sm_scale > 0.0f ? 1.0f : (a.sm_scale < 0.0f ? -1.0f : 0.0f);
@@ -497,15 +530,16 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     bool ok = true;
     while (ok && w.left > 0) {
       const int n = w.steps();
+      const int base0 = w.tile.lo + w.s0 * kTok;
       const int r0 = w.rt * kRows;
       const int rows = min(w.count * a.ratio - r0, kRows);
       const bool live_row = r < rows;
-      const int i_tok = (r0 + (live_row ? r : 0)) / a.ratio;
-      const int hq = w.h * a.ratio + (r0 + (live_row ? r : 0)) - i_tok * a.ratio;
       // ---- This row of Q.
       float f;
       int lo = 0, hi = 0;
       {
+        const int i_tok = (r0 + (live_row ? r : 0)) / a.ratio;
+        const int hq = w.h * a.ratio + (r0 + (live_row ? r : 0)) - i_tok * a.ratio;
         uint32_t raw[D / 2];
         const T* qp = static_cast<const T*>(a.q) + (w.first + i_tok) * a.q_token_stride + hq * a.q_head_stride;
         if (q_vec) {
@@ -535,7 +569,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
         e = e < -100 ? -100 : e;
         const float scale = sign * __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-        const uint32_t at = ptx::smem_u32(smem + L::offQ + m * L::kTile) + (r & 127) * 128;
+        const uint32_t at = ptx::smem_u32(smem + L::offQ + m * L::kTile) + in_tile * 128;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           // Elements 0 4, 1 5, 2 6, 3 7 of the block.
@@ -544,7 +578,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                                      attn::pack_half2(hi_of(x[0]) * scale, hi_of(x[2]) * scale),
                                      attn::pack_half2(lo_of(x[1]) * scale, lo_of(x[3]) * scale),
                                      attn::pack_half2(hi_of(x[1]) * scale, hi_of(x[3]) * scale));
-          ptx::sts128(at + (c >> 3) * L::kSub + (((c & 7) ^ (r & 7)) << 4), y);
+          ptx::sts128(at + (c >> 3) * L::kSub + (((c & 7) ^ (in_tile & 7)) << 4), y);
         }
         const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23) * (fabsf(a.sm_scale) * 1.4426950408889634f);
         f = sign == 0.0f ? 1.0f : fminf(fmaxf(f1, 0x1p-126f), 0x1p127f);
@@ -559,9 +593,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const int all_lo = __reduce_max_sync(0xffffffffu, live_row ? lo : 0);
       const int all_hi = __reduce_min_sync(0xffffffffu, live_row ? hi : 0x7FFFFFFF);
 
-      float mx = kNegInf, nmf = 0.0f;
+      float ref = kNegInf, nmf = 15.0f;  // the reference of S / f; x_run - ref * f
       float2 l = make_float2(0.0f, 0.0f);
       int x_run = 15;
+      bool bad_row = false;  // sees a value scale that is not finite: so is its output
       const float2 f2 = make_float2(f, f);
       for (int j = 0; j < n; ++j, ++t) {
         const int ring = t & (kScaleRing - 1);
@@ -571,99 +606,110 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         ptx::tc_fence_after();
         const float* const kc = s_scale + ring * 2 * kTok;
         const float* const vc = kc + kTok;
-        const int base = w.tile.lo + (w.s0 + j) * kTok;
-        const uint32_t live = s_bits[ring * 8] & s_bits[ring * 8 + 1] & s_bits[ring * 8 + 2] & s_bits[ring * 8 + 3];
-        const uint32_t bits = max(max(s_bits[ring * 8 + 4], s_bits[ring * 8 + 5]), max(s_bits[ring * 8 + 6], s_bits[ring * 8 + 7]));
-        const bool edge = base < all_lo || base + kTok > all_hi || live != 0xffffffffu;
-        // S / f of 32 columns from x: times the key scales, hidden tokens -inf.
-        auto scores = [&](int c, const uint32_t (&x)[32], float2 (&s)[16]) {
+        const int base = base0 + j * kTok;
+        const uint4 live = *reinterpret_cast<const uint4*>(s_bits[ring].live);
+        const uint4 bad = *reinterpret_cast<const uint4*>(s_bits[ring].bad);
+        const uint4 top4 = *reinterpret_cast<const uint4*>(s_bits[ring].top);
+        const int x_new = min(x_run, 21 - static_cast<int>(max(max(top4.x, top4.y), max(top4.z, top4.w)) >> 10));
+        // Which of the tokens this row sees, where it may not be all of them.
+        uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        const bool edge = base < all_lo || base + kTok > all_hi || (live.x & live.y & live.z & live.w) != 0xffffffffu;
+        if (edge) {
+          const uint32_t here[4] = {live.x, live.y, live.z, live.w};
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
+          for (int i = 0; i < 4; ++i) {
+            const int from = min(max(lo - (base + 32 * i), 0), 32), to = min(max(hi - (base + 32 * i), 0), 32);
+            const uint32_t below = to == 32 ? 0xffffffffu : (1u << to) - 1u;
+            seen[i] = from == 32 ? 0u : here[i] & below & (0xffffffffu << from);
+          }
+        }
+        if ((bad.x | bad.y | bad.z | bad.w) != 0u)
+          bad_row = bad_row || ((bad.x & seen[0]) | (bad.y & seen[1]) | (bad.z & seen[2]) | (bad.w & seen[3])) != 0u;
+        // W = 2^x P s of the 16 columns from c on, their sum, the maximum of S / f.
+        auto weights = [&](int c, uint32_t visible, const uint32_t (&x)[16], float2 nmf2, float2& sum, float2& top2,
+                           uint32_t (&pw)[8]) {
+          float2 s[8];
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
             const float4 k4 = *reinterpret_cast<const float4*>(kc + c + i);
             s[i / 2] = __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(k4.x, k4.y));
             s[i / 2 + 1] = __fmul2_rn(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(k4.z, k4.w));
           }
-          if (edge) {
-            const uint32_t here = s_bits[ring * 8 + c / 32];
+          if (__any_sync(0xffffffffu, (visible & 0xffffu) != 0xffffu)) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const int tok = base + c + i;
-              if (((here >> i) & 1u) == 0u || tok < lo || tok >= hi) s[i / 2].x = kNegInf;
-              if (((here >> (i + 1)) & 1u) == 0u || tok + 1 < lo || tok + 1 >= hi) s[i / 2].y = kNegInf;
+            for (int i = 0; i < 8; ++i) {
+              if (((visible >> (2 * i)) & 1u) == 0u) s[i].x = kNegInf;
+              if (((visible >> (2 * i + 1)) & 1u) == 0u) s[i].y = kNegInf;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const float4 v4 = *reinterpret_cast<const float4*>(vc + c + 2 * i);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              top2.x = fmaxf(top2.x, s[i + k].x);
+              top2.y = fmaxf(top2.y, s[i + k].y);
+              float2 p = __ffma2_rn(s[i + k], f2, nmf2);
+              p.x = attn::ex2(p.x);
+              p.y = attn::ex2(p.y);
+              sum = __fadd2_rn(sum, p);
+              const float2 y = __fmul2_rn(p, k == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
+              pw[i + k] = attn::pack_half2(y.x, y.y);
             }
           }
         };
-        // ---- The row's maximum over the tile.  S is read twice, 32 columns
-        // at a time with the next 32 on their way, and not kept in between.
-        float top = kNegInf;
+        // ---- Under the reference so far, kept in registers ...
+        float2 sum = make_float2(0.0f, 0.0f), top2 = make_float2(kNegInf, kNegInf);
+        uint32_t pw[kTok / 16][8];
         {
-          uint32_t x[2][32];
-          ptx::tmem_ld_32x32b_x32(s_at, x[0]);
+          const float2 nmf2 = make_float2(nmf, nmf);
+          uint32_t x[2][16];
+          ptx::tmem_ld_32x32b_x16(s_at, x[0]);
 #pragma unroll
-          for (int c = 0; c < kTok; c += 32) {
+          for (int c = 0; c < kTok; c += 16) {
             ptx::tmem_ld_wait();
-            if (c + 32 < kTok) ptx::tmem_ld_32x32b_x32(s_at + c + 32, x[(c / 32 + 1) & 1]);
-            float2 s[16];
-            scores(c, x[(c / 32) & 1], s);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(s[i].x, s[i].y));
+            if (c + 16 < kTok) ptx::tmem_ld_32x32b_x16(s_at + c + 16, x[(c / 16 + 1) & 1]);
+            weights(c, seen[c / 32] >> (c & 16), x[(c / 16) & 1], nmf2, sum, top2, pw[c / 16]);
           }
         }
-        // ---- The reference of the weights, when it is too far behind.
-        const int x_new = min(x_run, 21 - static_cast<int>(bits >> 10));
-        const bool behind = top > mx && (mx == kNegInf || (top - mx) * f > kGrow);
-        if (__any_sync(0xffffffffu, behind) || x_new != x_run) {
-          const float m_new = fmaxf(mx, top);
-          float al = m_new == mx ? 1.0f : attn::ex2((mx - m_new) * f);
+        const float top = fmaxf(top2.x, top2.y);
+        const bool behind = top > ref && (ref == kNegInf || (top - ref) * f > kGrow);
+        if (!__any_sync(0xffffffffu, behind) && x_new == x_run) {
+#pragma unroll
+          for (int c = 0; c < kTok / 16; ++c) tmem_st_32x32b_x8(s_at + 8 * c, pw[c]);
+        } else {
+          // ---- ... or, when the maximum has left it too far behind, under a
+          // new one, from S again, W following over the columns that were read.
+          const float new_ref = fmaxf(ref, top);
+          float al = new_ref == ref ? 1.0f : attn::ex2((ref - new_ref) * f);
           al *= __uint_as_float(static_cast<uint32_t>(127 + x_new - x_run) << 23);
-          mx = m_new;
+          ref = new_ref;
           x_run = x_new;
-          nmf = static_cast<float>(x_run) - (mx == kNegInf ? 0.0f : mx * f);
+          nmf = static_cast<float>(x_run) - (ref == kNegInf ? 0.0f : ref * f);
           l = __fmul2_rn(l, make_float2(al, al));
           if (j > 0) {  // the products of all earlier tiles are complete: S came after them
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 16) {
-              uint32_t x[16];
-              ptx::tmem_ld_32x32b_x16(o_at + c, x);
+              uint32_t y[16];
+              ptx::tmem_ld_32x32b_x16(o_at + c, y);
               ptx::tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * al);
-              tmem_st_32x32b_x16(o_at + c, x);
+              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * al);
+              tmem_st_32x32b_x16(o_at + c, y);
             }
           }
-        }
-        // ---- W = 2^x P s, over the columns of S.
-        const float2 nmf2 = make_float2(nmf, nmf);
-        {
-          uint32_t x[2][32];
-          ptx::tmem_ld_32x32b_x32(s_at, x[0]);
-#pragma unroll
-          for (int c = 0; c < kTok; c += 32) {
+          sum = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+          for (int c = 0; c < kTok; c += 16) {
+            uint32_t x[16], y[8];
+            ptx::tmem_ld_32x32b_x16(s_at + c, x);
             ptx::tmem_ld_wait();
-            if (c + 32 < kTok) ptx::tmem_ld_32x32b_x32(s_at + c + 32, x[(c / 32 + 1) & 1]);
-            float2 s[16];
-            scores(c, x[(c / 32) & 1], s);
-            uint32_t pw[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 v4 = *reinterpret_cast<const float4*>(vc + c + i);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float2 p = __ffma2_rn(s[i / 2 + k], f2, nmf2);
-                p.x = attn::ex2(p.x);
-                p.y = attn::ex2(p.y);
-                l = __fadd2_rn(l, p);
-                float2 y = __fmul2_rn(p, k == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
-                if (edge) {  // a hidden token's weight is 0 under any scale
-                  y.x = p.x == 0.0f ? 0.0f : y.x;
-                  y.y = p.y == 0.0f ? 0.0f : y.y;
-                }
-                pw[i / 2 + k] = attn::pack_half2(y.x, y.y);
-              }
-            }
-            tmem_st_32x32b_x16(s_at + c / 2, pw);  // over columns that have been read
+            const uint32_t word = c < 64 ? (c < 32 ? seen[0] : seen[1]) : (c < 96 ? seen[2] : seen[3]);
+            weights(c, word >> (c & 16), x, make_float2(nmf, nmf), sum, top2, y);
+            tmem_st_32x32b_x8(s_at + c / 2, y);
           }
         }
+        l = __fadd2_rn(l, sum);
         tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
@@ -675,18 +721,20 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       ptx::tc_fence_after();
       const bool whole = n == w.tile.steps;
       const float sum = l.x + l.y;
-      const int at = (w.first + i_tok) * a.q_heads + hq;
+      const int i_tok = (r0 + (live_row ? r : 0)) / a.ratio;
+      const int at = (w.first + i_tok) * a.q_heads + w.h * a.ratio + (r0 + (live_row ? r : 0)) - i_tok * a.ratio;
       const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (w.s0 == 0 ? 1 : 0)) * kRows + r;
       const float back = __uint_as_float(static_cast<uint32_t>(127 - x_run) << 23);
-      const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : back;
+      float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : back;
+      if (bad_row) inv = __int_as_float(0x7FC00000);
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t x[32];
-        ptx::tmem_ld_32x32b_x32(o_at + c, x);
+      for (int c = 0; c < D; c += 16) {
+        uint32_t x[16];
+        ptx::tmem_ld_32x32b_x16(o_at + c, x);
         ptx::tmem_ld_wait();
         if (live_row) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
+          for (int i = 0; i < 16; i += 8) {
             float v[8];  // columns 0 .. 7 of a block are its elements 0 4 1 5 2 6 3 7
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[(k >> 1) + 4 * (k & 1)] = __uint_as_float(x[i + k]) * inv;
@@ -705,7 +753,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         }
       }
       if (live_row) {
-        const float top = mx * f;
+        const float top = ref * f;
         if (!whole) {
           ws.ml[slot * 2] = top;
           ws.ml[slot * 2 + 1] = sum * back;
@@ -715,7 +763,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         }
       }
       ++item;
-      w.next(a);
+      walk_next();
     }
     if (ok) {  // no more items
       if (warp == 8) s_steps[item & 1u] = 0;
