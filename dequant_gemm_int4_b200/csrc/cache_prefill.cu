@@ -1,22 +1,23 @@
 // Attention over the 4-bit cache for many query rows (prompts in chunks), on
 // the tcgen05 tensor cores (sm_100a).
 //
-// Same operator, split over the lengths and joining kernel as the kernel for
-// few rows (cache_attention.cuh); here a block's item is 256 query rows of one
-// key/value head, two MMA tiles of 128 rows that share every key and value
-// tile of 128 tokens:
-//   S_m = Q_m K^T         128 x 128 x D, both operands in shared memory
-//   O_m += W_m V          128 x D x 128, W from tensor memory
-// Tensor memory holds S_0, S_1 (fp32, 128 columns each; W_m, fp16, overlays the
-// the first half of S_m once S_m has been read) and O_0, O_1 (D columns each).
+// Same operator and split over the lengths as the kernel for few rows
+// (cache_attention.cuh); here a block's item is 256 query rows of one key/value
+// head, two MMA tiles of 128 rows that share every tile of 128 tokens, taken in
+// two halves:
+//   S_m = Q_m K^T         128 x 64 x D, both operands in shared memory
+//   O_m += W_m V          128 x D x 64, W from tensor memory
+// Tensor memory holds two buffers of S for each m (fp32, 64 columns; W_m, fp16,
+// overlays the first half of its S once that has been read) and O_0, O_1 (D
+// columns each).  So S of the next half tile is ready before the softmax of
+// this one has ended: with one buffer of 128 columns, S waited for W V of the
+// same columns, and the chain S, softmax, W V took 2.2 times as long.
 //
 // Roles of the block's 16 warps:
 //   warps 0-3    warp 0 issues the MMAs; the others only lend their registers
 //   warps 4-7    expand codes: thread t owns token t of the tile, its key row
 //                and its value row
 //   warps 8-15   softmax: thread r of group m owns query row r of tile m
-// The issue order S_0(j+1) behind W_0(j) V, S_1(j+1) behind W_1(j) V lets each
-// group's softmax run under the other group's MMAs.
 //
 // Operands are exact: q in fp16 after a power-of-two scaling of its row (see
 // cache_attention.cuh), keys and values as the integers n - z.  The token's
@@ -53,7 +54,8 @@ constexpr uint64_t kWaitNs = 250000000ull;  // far above any legitimate wait
 struct Bars {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t sc_full[kScaleRing];
-  uint64_t s_full[2], w_full[2];  // per row tile: S computed; W stored
+  uint64_t s_full[2][2], w_full[2][2];  // per row tile and buffer: S computed; W stored
+  uint64_t o_done[2];                   // per row tile: W V added
   uint64_t q_full, o_full;        // per item
   uint64_t drain;
 };
@@ -195,8 +197,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       ptx::mbar_init(bar(bars->k_empty[i]), 1);
       ptx::mbar_init(bar(bars->v_full[i]), 4);
       ptx::mbar_init(bar(bars->v_empty[i]), 1);
-      ptx::mbar_init(bar(bars->s_full[i]), 1);
-      ptx::mbar_init(bar(bars->w_full[i]), 4);
+      for (int k = 0; k < 2; ++k) {
+        ptx::mbar_init(bar(bars->s_full[i][k]), 1);
+        ptx::mbar_init(bar(bars->w_full[i][k]), 4);
+      }
+      ptx::mbar_init(bar(bars->o_done[i]), 1);
     }
     for (int i = 0; i < kScaleRing; ++i) ptx::mbar_init(bar(bars->sc_full[i]), 4);
     ptx::mbar_init(bar(bars->q_full), 8);
@@ -346,28 +351,30 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     if (warp == 0) {
       // ---------------- MMA issuer ----------------
       const bool leader = ptx::elect_one();
-      constexpr uint32_t id_s = instr_desc(kTok, false), id_o = instr_desc(D, true);
+      constexpr uint32_t id_s = instr_desc(64, false), id_o = instr_desc(D, true);
       const uint32_t q_at = ptx::smem_u32(smem + L::offQ), k_at = ptx::smem_u32(smem + L::offK),
                      v_at = ptx::smem_u32(smem + L::offV);
-      auto s_mma = [&](int m, int stage) {
+      // Half `h` of a stage's tokens lies 64 rows of 128 bytes on.
+      auto s_mma = [&](int m, int stage, int h) {
         if (leader) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = (k / 4) * L::kSub + (k % 4) * 32;
-            ptx::umma_f16(tmem + m * kTok, ptx::sw128_kmajor_desc(q_at + m * L::kTile + off),
-                          ptx::sw128_kmajor_desc(k_at + stage * L::kTile + off), id_s, k == 0 ? 0u : 1u);
+            ptx::umma_f16(tmem + m * kTok + h * 64, ptx::sw128_kmajor_desc(q_at + m * L::kTile + off),
+                          ptx::sw128_kmajor_desc(k_at + stage * L::kTile + h * 8192 + off), id_s, k == 0 ? 0u : 1u);
           }
-          ptx::umma_commit(bar(bars->s_full[m]));
+          ptx::umma_commit(bar(bars->s_full[m][h]));
         }
         __syncwarp();
       };
-      auto o_mma = [&](int m, int stage, bool first) {
+      auto o_mma = [&](int m, int stage, int h, bool first) {
         if (leader) {
 #pragma unroll
-          for (int k = 0; k < kTok / 16; ++k)
-            umma_f16_ts(tmem + 2 * kTok + m * D, tmem + m * kTok + 8 * k,
-                        sw128_mnmajor_desc(v_at + stage * L::kTile + k * 2048, L::kSub), id_o,
+          for (int k = 0; k < 4; ++k)
+            umma_f16_ts(tmem + 2 * kTok + m * D, tmem + m * kTok + h * 64 + 8 * k,
+                        sw128_mnmajor_desc(v_at + stage * L::kTile + h * 8192 + k * 2048, L::kSub), id_o,
                         first && k == 0 ? 0u : 1u);
+          ptx::umma_commit(bar(bars->o_done[m]));
         }
         __syncwarp();
       };
@@ -380,25 +387,26 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (n == 0) break;
         if (!(ok = wait_all(bar(bars->k_full[t & 1]), (t >> 1) & 1u, wc))) break;
         ptx::tc_fence_after();
-        s_mma(0, t & 1);
-        s_mma(1, t & 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_mma(i & 1, t & 1, i >> 1);
         if (leader) ptx::umma_commit(bar(bars->k_empty[t & 1]));
         __syncwarp();
         for (int j = 0; ok && j < n; ++j, ++t) {
           ok = wait_all(bar(bars->v_full[t & 1]), (t >> 1) & 1u, wc);
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            ok = ok && wait_all(bar(bars->w_full[m]), t & 1u, wc);
+          for (int i = 0; i < 4; ++i) {
+            const int m = i & 1, h = i >> 1;
+            ok = ok && wait_all(bar(bars->w_full[m][h]), t & 1u, wc);
             if (!ok) break;
             ptx::tc_fence_after();
-            o_mma(m, t & 1, j == 0);
-            if (j + 1 < n) {
-              if (m == 0) {
+            o_mma(m, t & 1, h, j == 0 && h == 0);
+            if (j + 1 < n) {  // S of the next tile into the buffer that W V has just read
+              if (i == 0) {
                 ok = wait_all(bar(bars->k_full[(t + 1) & 1]), ((t + 1) >> 1) & 1u, wc);
                 if (!ok) break;
                 ptx::tc_fence_after();
               }
-              s_mma(m, (t + 1) & 1);
+              s_mma(m, (t + 1) & 1, h);
             }
           }
           if (!ok) break;
@@ -522,7 +530,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const int q4 = warp & 3;                 // lanes of tensor memory this warp reads
     const int in_tile = q4 * 32 + lane, r = m * 128 + in_tile;  // row of the item
     const uint32_t lane_at = tmem + (static_cast<uint32_t>(32 * q4) << 16);
-    const uint32_t s_at = lane_at + m * kTok, o_at = lane_at + 2 * kTok + m * D;
+    const uint32_t o_at = lane_at + 2 * kTok + m * D;
     const float sign = a.sm_scale > 0.0f ? 1.0f : (a.sm_scale < 0.0f ? -1.0f : 0.0f);
     const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_token_stride % 8 == 0 && a.q_head_stride % 8 == 0;
     int t = 0;
@@ -598,33 +606,32 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       int x_run = 15;
       bool bad_row = false;  // sees a value scale that is not finite: so is its output
       const float2 f2 = make_float2(f, f);
-      for (int j = 0; j < n; ++j, ++t) {
-        const int ring = t & (kScaleRing - 1);
-        ok = wait_all(bar(bars->sc_full[ring]), (t / kScaleRing) & 1u, wc) &&
-             wait_all(bar(bars->s_full[m]), t & 1u, wc);
+      for (int u = 0; u < 2 * n; ++u) {  // half tiles
+        const int h = u & 1, ring = t & (kScaleRing - 1);
+        ok = (h == 1 || wait_all(bar(bars->sc_full[ring]), (t / kScaleRing) & 1u, wc)) &&
+             wait_all(bar(bars->s_full[m][h]), t & 1u, wc);
         if (!ok) break;
         ptx::tc_fence_after();
-        const float* const kc = s_scale + ring * 2 * kTok;
+        const uint32_t s_at = lane_at + m * kTok + h * 64;
+        const float* const kc = s_scale + ring * 2 * kTok + h * 64;
         const float* const vc = kc + kTok;
-        const int base = base0 + j * kTok;
-        const uint4 live = *reinterpret_cast<const uint4*>(s_bits[ring].live);
-        const uint4 bad = *reinterpret_cast<const uint4*>(s_bits[ring].bad);
-        const uint4 top4 = *reinterpret_cast<const uint4*>(s_bits[ring].top);
-        const int x_new = min(x_run, 21 - static_cast<int>(max(max(top4.x, top4.y), max(top4.z, top4.w)) >> 10));
+        const int base = base0 + u * 64;
+        const uint2 live = *reinterpret_cast<const uint2*>(s_bits[ring].live + 2 * h);
+        const uint2 bad = *reinterpret_cast<const uint2*>(s_bits[ring].bad + 2 * h);
+        const uint2 top2u = *reinterpret_cast<const uint2*>(s_bits[ring].top + 2 * h);
+        const int x_new = min(x_run, 21 - static_cast<int>(max(top2u.x, top2u.y) >> 10));
         // Which of the tokens this row sees, where it may not be all of them.
-        uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-        const bool edge = base < all_lo || base + kTok > all_hi || (live.x & live.y & live.z & live.w) != 0xffffffffu;
-        if (edge) {
-          const uint32_t here[4] = {live.x, live.y, live.z, live.w};
+        uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+        if (base < all_lo || base + 64 > all_hi || (live.x & live.y) != 0xffffffffu) {
+          const uint32_t here[2] = {live.x, live.y};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i) {
             const int from = min(max(lo - (base + 32 * i), 0), 32), to = min(max(hi - (base + 32 * i), 0), 32);
             const uint32_t below = to == 32 ? 0xffffffffu : (1u << to) - 1u;
             seen[i] = from == 32 ? 0u : here[i] & below & (0xffffffffu << from);
           }
         }
-        if ((bad.x | bad.y | bad.z | bad.w) != 0u)
-          bad_row = bad_row || ((bad.x & seen[0]) | (bad.y & seen[1]) | (bad.z & seen[2]) | (bad.w & seen[3])) != 0u;
+        if ((bad.x | bad.y) != 0u) bad_row = bad_row || ((bad.x & seen[0]) | (bad.y & seen[1])) != 0u;
         // W = 2^x P s of the 16 columns from c on, their sum, the maximum of S / f.
         auto weights = [&](int c, uint32_t visible, const uint32_t (&x)[16], float2 nmf2, float2& sum, float2& top2,
                            uint32_t (&pw)[8]) {
@@ -660,23 +667,21 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         };
         // ---- Under the reference so far, kept in registers ...
         float2 sum = make_float2(0.0f, 0.0f), top2 = make_float2(kNegInf, kNegInf);
-        uint32_t pw[kTok / 16][8];
+        uint32_t pw[4][8];
         {
           const float2 nmf2 = make_float2(nmf, nmf);
-          uint32_t x[2][16];
-          ptx::tmem_ld_32x32b_x16(s_at, x[0]);
+          uint32_t x[4][16];
 #pragma unroll
-          for (int c = 0; c < kTok; c += 16) {
-            ptx::tmem_ld_wait();
-            if (c + 16 < kTok) ptx::tmem_ld_32x32b_x16(s_at + c + 16, x[(c / 16 + 1) & 1]);
-            weights(c, seen[c / 32] >> (c & 16), x[(c / 16) & 1], nmf2, sum, top2, pw[c / 16]);
-          }
+          for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x16(s_at + 16 * c, x[c]);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) weights(16 * c, seen[c / 2] >> (16 * (c & 1)), x[c], nmf2, sum, top2, pw[c]);
         }
         const float top = fmaxf(top2.x, top2.y);
         const bool behind = top > ref && (ref == kNegInf || (top - ref) * f > kGrow);
         if (!__any_sync(0xffffffffu, behind) && x_new == x_run) {
 #pragma unroll
-          for (int c = 0; c < kTok / 16; ++c) tmem_st_32x32b_x8(s_at + 8 * c, pw[c]);
+          for (int c = 0; c < 4; ++c) tmem_st_32x32b_x8(s_at + 8 * c, pw[c]);
         } else {
           // ---- ... or, when the maximum has left it too far behind, under a
           // new one, from S again, W following over the columns that were read.
@@ -687,7 +692,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           x_run = x_new;
           nmf = static_cast<float>(x_run) - (ref == kNegInf ? 0.0f : ref * f);
           l = __fmul2_rn(l, make_float2(al, al));
-          if (j > 0) {  // the products of all earlier tiles are complete: S came after them
+          if (u > 0) {
+            // The products of the half tile before are still being added, or
+            // their turn has not come.
+            if (!(ok = wait_all(bar(bars->o_done[m]), (2 * t + h - 1) & 1u, wc))) break;
+            ptx::tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t y[16];
@@ -700,12 +709,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           }
           sum = make_float2(0.0f, 0.0f);
 #pragma unroll 1
-          for (int c = 0; c < kTok; c += 16) {
+          for (int c = 0; c < 64; c += 16) {
             uint32_t x[16], y[8];
             ptx::tmem_ld_32x32b_x16(s_at + c, x);
             ptx::tmem_ld_wait();
-            const uint32_t word = c < 64 ? (c < 32 ? seen[0] : seen[1]) : (c < 96 ? seen[2] : seen[3]);
-            weights(c, word >> (c & 16), x, make_float2(nmf, nmf), sum, top2, y);
+            weights(c, (c < 32 ? seen[0] : seen[1]) >> (c & 16), x, make_float2(nmf, nmf), sum, top2, y);
             tmem_st_32x32b_x8(s_at + c / 2, y);
           }
         }
@@ -713,7 +721,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(bars->w_full[m]));
+        if (lane == 0) ptx::mbar_arrive(bar(bars->w_full[m][h]));
+        t += h;
       }
       if (!ok) break;
       // ---- O.
