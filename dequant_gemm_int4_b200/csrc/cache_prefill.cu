@@ -74,27 +74,45 @@ struct Smem {
   static constexpr int kAlloc = offMisc + 64 + 1024;  // slack to align the base to 1024
 };
 
-// Operand stored with rows along K and 128-byte swizzle, read with its
-// contiguous dimension along N: 8 rows of an atom `8 * 128` bytes apart along
-// K (stride offset), atoms of 64 elements kSub bytes apart along N (leading
-// offset).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t atom_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(atom_bytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
+// Shared-memory descriptors of operands with the 128-byte swizzle, built from
+// a low word, in which tiles differ by their address alone (an addition of
+// bytes / 16), and a constant high word.  K along the rows' 128 bytes: as
+// ptx::sw128_kmajor_desc.  N along them (the value tile): 8 rows of an atom
+// along K, atoms 1024 bytes apart (stride offset); atoms of 64 elements along N
+// `atom_bytes` apart (leading offset).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t atom_bytes) {
+  return ((addr & 0x3FFFFu) >> 4) | ((atom_bytes >> 4) << 16);
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t desc_at(uint32_t lo, uint32_t bytes) {
+  return (static_cast<uint64_t>(kDescHi) << 32) | (lo + (bytes >> 4));
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16, one CTA.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// D[tmem] (+)= A * B[smem desc], kind::f16, one CTA, A from shared or tensor
+// memory; issued by the lane whose `lead` is 1.  Predicated rather than inside
+// a branch of one lane: the code around stays uniform, and the operands in
+// uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+// Arrive once on `bar` when all MMAs that this lane has issued are complete.
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar), "r"(lead)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -350,33 +368,29 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     ptx::regs_dec<40>();
     if (warp == 0) {
       // ---------------- MMA issuer ----------------
-      const bool leader = ptx::elect_one();
+      const uint32_t lead = ptx::elect_one() ? 1u : 0u;
       constexpr uint32_t id_s = instr_desc(64, false), id_o = instr_desc(D, true);
-      const uint32_t q_at = ptx::smem_u32(smem + L::offQ), k_at = ptx::smem_u32(smem + L::offK),
-                     v_at = ptx::smem_u32(smem + L::offV);
+      // The leading offset of K-major operands is not used (1, as elsewhere).
+      const uint32_t q_lo = desc_lo(ptx::smem_u32(smem + L::offQ), 16), k_lo0 = desc_lo(ptx::smem_u32(smem + L::offK), 16),
+                     v_lo0 = desc_lo(ptx::smem_u32(smem + L::offV), L::kSub);
       // Half `h` of a stage's tokens lies 64 rows of 128 bytes on.
       auto s_mma = [&](int m, int stage, int h) {
-        if (leader) {
+        const uint32_t k_lo = k_lo0 + stage * (L::kTile >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * L::kSub + (k % 4) * 32;
-            ptx::umma_f16(tmem + m * kTok + h * 64, ptx::sw128_kmajor_desc(q_at + m * L::kTile + off),
-                          ptx::sw128_kmajor_desc(k_at + stage * L::kTile + h * 8192 + off), id_s, k == 0 ? 0u : 1u);
-          }
-          ptx::umma_commit(bar(bars->s_full[m][h]));
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * L::kSub + (k % 4) * 32;
+          mma_ss(lead, tmem + m * kTok + h * 64, desc_at(q_lo, m * L::kTile + off), desc_at(k_lo, h * 8192 + off), id_s,
+                 k == 0 ? 0u : 1u);
         }
-        __syncwarp();
+        commit(lead, bar(bars->s_full[m][h]));
       };
       auto o_mma = [&](int m, int stage, int h, bool first) {
-        if (leader) {
+        const uint32_t v_lo = v_lo0 + stage * (L::kTile >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_f16_ts(tmem + 2 * kTok + m * D, tmem + m * kTok + h * 64 + 8 * k,
-                        sw128_mnmajor_desc(v_at + stage * L::kTile + h * 8192 + k * 2048, L::kSub), id_o,
-                        first && k == 0 ? 0u : 1u);
-          ptx::umma_commit(bar(bars->o_done[m]));
-        }
-        __syncwarp();
+        for (int k = 0; k < 4; ++k)
+          mma_ts(lead, tmem + 2 * kTok + m * D, tmem + m * kTok + h * 64 + 8 * k, desc_at(v_lo, h * 8192 + k * 2048), id_o,
+                 first && k == 0 ? 0u : 1u);
+        commit(lead, bar(bars->o_done[m]));
       };
       int t = 0;  // tiles before this one
       uint32_t item = 0;
@@ -389,8 +403,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         ptx::tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 4; ++i) s_mma(i & 1, t & 1, i >> 1);
-        if (leader) ptx::umma_commit(bar(bars->k_empty[t & 1]));
-        __syncwarp();
+        commit(lead, bar(bars->k_empty[t & 1]));
         for (int j = 0; ok && j < n; ++j, ++t) {
           ok = wait_all(bar(bars->v_full[t & 1]), (t >> 1) & 1u, wc);
 #pragma unroll
@@ -400,29 +413,31 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             if (!ok) break;
             ptx::tc_fence_after();
             o_mma(m, t & 1, h, j == 0 && h == 0);
-            if (j + 1 < n) {  // S of the next tile into the buffer that W V has just read
-              if (i == 0) {
+            // Then S into the buffer that the W V before this one has read, one
+            // step behind, so that it does not wait for it.
+            if (i == 0) {
+              if (j > 0) {
+                s_mma(1, t & 1, 1);
+                commit(lead, bar(bars->k_empty[t & 1]));
+              }
+            } else if (j + 1 < n) {
+              if (i == 1) {
                 ok = wait_all(bar(bars->k_full[(t + 1) & 1]), ((t + 1) >> 1) & 1u, wc);
                 if (!ok) break;
                 ptx::tc_fence_after();
               }
-              s_mma(m, (t + 1) & 1, h);
+              s_mma((i - 1) & 1, (t + 1) & 1, (i - 1) >> 1);
             }
           }
           if (!ok) break;
-          if (leader) {
-            ptx::umma_commit(bar(bars->v_empty[t & 1]));
-            if (j + 1 < n) ptx::umma_commit(bar(bars->k_empty[(t + 1) & 1]));
-            else ptx::umma_commit(bar(bars->o_full));
-          }
-          __syncwarp();
+          commit(lead, bar(bars->v_empty[t & 1]));
+          if (j + 1 == n) commit(lead, bar(bars->o_full));
         }
         if (!ok) break;
         ++item;
       }
       if (*abort_flag) {  // nothing may be in flight when tensor memory is freed
-        if (leader) ptx::umma_commit(bar(bars->drain));
-        __syncwarp();
+        commit(lead, bar(bars->drain));
         const uint64_t t0 = ptx::globaltimer();
         for (uint32_t i = 0; i != 0xFFFFFFFFu; ++i) {
           if (ptx::mbar_try_wait(bar(bars->drain), 0)) break;
