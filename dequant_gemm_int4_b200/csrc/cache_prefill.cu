@@ -26,9 +26,9 @@
 // So one group a head is required here (group = head_dim).  S, the maximum and
 // the sum are fp32; O is fp32 in tensor memory.  Weights are taken relative to a
 // reference that follows the row's maximum only when that has passed it by
-// more than a factor 2^8: a tile's weights are computed at once under the old
-// reference, and again, after O has been rescaled, in the rare tile that
-// turns out to need a new one.
+// more than a factor 2^8: a half tile's weights are computed at once under the
+// old reference, and only where that turns out too far behind, or some row
+// does not see all tokens, with the maximum first.
 //
 // Inside blocks of 8 elements, keys and queries are stored in the order 0, 4,
 // 1, 5, 2, 6, 3, 7 in which a code word expands pair by pair; O's columns come
@@ -635,42 +635,22 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const uint2 bad = *reinterpret_cast<const uint2*>(s_bits[ring].bad + 2 * h);
         const uint2 top2u = *reinterpret_cast<const uint2*>(s_bits[ring].top + 2 * h);
         const int x_new = min(x_run, 21 - static_cast<int>(max(top2u.x, top2u.y) >> 10));
-        // Which of the tokens this row sees, where it may not be all of them.
-        uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
-        if (base < all_lo || base + 64 > all_hi || (live.x & live.y) != 0xffffffffu) {
-          const uint32_t here[2] = {live.x, live.y};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int from = min(max(lo - (base + 32 * i), 0), 32), to = min(max(hi - (base + 32 * i), 0), 32);
-            const uint32_t below = to == 32 ? 0xffffffffu : (1u << to) - 1u;
-            seen[i] = from == 32 ? 0u : here[i] & below & (0xffffffffu << from);
-          }
-        }
-        if ((bad.x | bad.y) != 0u) bad_row = bad_row || ((bad.x & seen[0]) | (bad.y & seen[1])) != 0u;
-        // W = 2^x P s of the 16 columns from c on, their sum, the maximum of S / f.
-        auto weights = [&](int c, uint32_t visible, const uint32_t (&x)[16], float2 nmf2, float2& sum, float2& top2,
-                           uint32_t (&pw)[8]) {
-          float2 s[8];
+        // Scores of the 16 columns from c on: S / f.
+        auto scores = [&](int c, const uint32_t (&x)[16], float2 (&s)[8]) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             const float4 k4 = *reinterpret_cast<const float4*>(kc + c + i);
             s[i / 2] = __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(k4.x, k4.y));
             s[i / 2 + 1] = __fmul2_rn(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(k4.z, k4.w));
           }
-          if (__any_sync(0xffffffffu, (visible & 0xffffu) != 0xffffu)) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (((visible >> (2 * i)) & 1u) == 0u) s[i].x = kNegInf;
-              if (((visible >> (2 * i + 1)) & 1u) == 0u) s[i].y = kNegInf;
-            }
-          }
+        };
+        // Their weights W = 2^x P s, and the weights' sum without s.
+        auto weights = [&](int c, const float2 (&s)[8], float2 nmf2, float2& sum, uint32_t (&pw)[8]) {
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const float4 v4 = *reinterpret_cast<const float4*>(vc + c + 2 * i);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              top2.x = fmaxf(top2.x, s[i + k].x);
-              top2.y = fmaxf(top2.y, s[i + k].y);
               float2 p = __ffma2_rn(s[i + k], f2, nmf2);
               p.x = attn::ex2(p.x);
               p.y = attn::ex2(p.y);
@@ -680,55 +660,105 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             }
           }
         };
-        // ---- Under the reference so far, kept in registers ...
-        float2 sum = make_float2(0.0f, 0.0f), top2 = make_float2(kNegInf, kNegInf);
-        uint32_t pw[4][8];
-        {
+        float2 sum = make_float2(0.0f, 0.0f);
+        const bool edge = base < all_lo || base + 64 > all_hi || (live.x & live.y) != 0xffffffffu;
+        bool slow = edge || x_new != x_run || (bad.x | bad.y) != 0u;
+        if (!slow) {
+          // ---- All rows see all tokens: the weights under the reference so
+          // far, in registers until it has proved near enough.  One piece of
+          // straight code, so that its 64 columns overlap.
+          float2 top2[2] = {make_float2(kNegInf, kNegInf), make_float2(kNegInf, kNegInf)};
           const float2 nmf2 = make_float2(nmf, nmf);
-          uint32_t x[4][16];
+          uint32_t x[4][16], pw[4][8];
 #pragma unroll
           for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x16(s_at + 16 * c, x[c]);
           ptx::tmem_ld_wait();
+          float2 part[2] = {sum, sum};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) weights(16 * c, seen[c / 2] >> (16 * (c & 1)), x[c], nmf2, sum, top2, pw[c]);
+          for (int c = 0; c < 4; ++c) {
+            float2 s[8];
+            scores(16 * c, x[c], s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              top2[i & 1].x = fmaxf(top2[i & 1].x, s[i].x);
+              top2[i & 1].y = fmaxf(top2[i & 1].y, s[i].y);
+            }
+            weights(16 * c, s, nmf2, part[c & 1], pw[c]);
+          }
+          sum = __fadd2_rn(part[0], part[1]);
+          const float top = fmaxf(fmaxf(top2[0].x, top2[0].y), fmaxf(top2[1].x, top2[1].y));
+          slow = __any_sync(0xffffffffu, top > ref && (ref == kNegInf || (top - ref) * f > kGrow));
+          if (!slow) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_st_32x32b_x8(s_at + 8 * c, pw[c]);
+          }
         }
-        const float top = fmaxf(top2.x, top2.y);
-        const bool behind = top > ref && (ref == kNegInf || (top - ref) * f > kGrow);
-        if (!__any_sync(0xffffffffu, behind) && x_new == x_run) {
+        if (slow) {
+          // ---- Otherwise the maximum first, of the tokens that the row sees.
+          uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+          if (edge) {
+            const uint32_t here[2] = {live.x, live.y};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_st_32x32b_x8(s_at + 8 * c, pw[c]);
-        } else {
-          // ---- ... or, when the maximum has left it too far behind, under a
-          // new one, from S again, W following over the columns that were read.
-          const float new_ref = fmaxf(ref, top);
-          float al = new_ref == ref ? 1.0f : attn::ex2((ref - new_ref) * f);
-          al *= __uint_as_float(static_cast<uint32_t>(127 + x_new - x_run) << 23);
-          ref = new_ref;
-          x_run = x_new;
-          nmf = static_cast<float>(x_run) - (ref == kNegInf ? 0.0f : ref * f);
-          l = __fmul2_rn(l, make_float2(al, al));
-          if (u > 0) {
-            // The products of the half tile before are still being added, or
-            // their turn has not come.
-            if (!(ok = wait_all(bar(bars->o_done[m]), (2 * t + h - 1) & 1u, wc))) break;
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t y[16];
-              ptx::tmem_ld_32x32b_x16(o_at + c, y);
-              ptx::tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * al);
-              tmem_st_32x32b_x16(o_at + c, y);
+            for (int i = 0; i < 2; ++i) {
+              const int from = min(max(lo - (base + 32 * i), 0), 32), to = min(max(hi - (base + 32 * i), 0), 32);
+              const uint32_t below = to == 32 ? 0xffffffffu : (1u << to) - 1u;
+              seen[i] = from == 32 ? 0u : here[i] & below & (0xffffffffu << from);
             }
           }
+          if ((bad.x | bad.y) != 0u) bad_row = bad_row || ((bad.x & seen[0]) | (bad.y & seen[1])) != 0u;
+          auto load = [&](int c, float2 (&s)[8]) {
+            uint32_t x[16];
+            ptx::tmem_ld_32x32b_x16(s_at + c, x);
+            ptx::tmem_ld_wait();
+            scores(c, x, s);
+            const uint32_t visible = (c < 32 ? seen[0] : seen[1]) >> (c & 16);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (((visible >> (2 * i)) & 1u) == 0u) s[i].x = kNegInf;
+              if (((visible >> (2 * i + 1)) & 1u) == 0u) s[i].y = kNegInf;
+            }
+          };
+          float top = kNegInf;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 16) {
+            float2 s[8];
+            load(c, s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(s[i].x, s[i].y));
+          }
+          const bool behind = top > ref && (ref == kNegInf || (top - ref) * f > kGrow);
+          if (__any_sync(0xffffffffu, behind) || x_new != x_run) {
+            const float new_ref = fmaxf(ref, top);
+            float al = new_ref == ref ? 1.0f : attn::ex2((ref - new_ref) * f);
+            al *= __uint_as_float(static_cast<uint32_t>(127 + x_new - x_run) << 23);
+            ref = new_ref;
+            x_run = x_new;
+            nmf = static_cast<float>(x_run) - (ref == kNegInf ? 0.0f : ref * f);
+            l = __fmul2_rn(l, make_float2(al, al));
+            if (u > 0) {
+              // The products of the half tile before are still being added, or
+              // their turn has not come.
+              if (!(ok = wait_all(bar(bars->o_done[m]), (2 * t + h - 1) & 1u, wc))) break;
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t y[16];
+                ptx::tmem_ld_32x32b_x16(o_at + c, y);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * al);
+                tmem_st_32x32b_x16(o_at + c, y);
+              }
+            }
+          }
+          // W follows over the columns of S that have been read.
           sum = make_float2(0.0f, 0.0f);
 #pragma unroll 1
           for (int c = 0; c < 64; c += 16) {
-            uint32_t x[16], y[8];
-            ptx::tmem_ld_32x32b_x16(s_at + c, x);
-            ptx::tmem_ld_wait();
-            weights(c, (c < 32 ? seen[0] : seen[1]) >> (c & 16), x, make_float2(nmf, nmf), sum, top2, y);
+            float2 s[8];
+            uint32_t y[8];
+            load(c, s);
+            weights(c, s, make_float2(nmf, nmf), sum, y);
             tmem_st_32x32b_x8(s_at + c / 2, y);
           }
         }
