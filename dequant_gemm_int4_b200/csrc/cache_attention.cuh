@@ -208,12 +208,6 @@ __device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
   asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Halves of r are zeroed where those of p are zero.
-__device__ __forceinline__ uint32_t zero_where_zero(uint32_t r, uint32_t p) {
-  if ((p & 0x7FFFu) == 0u) r &= 0xFFFF0000u;
-  if ((p & 0x7FFF0000u) == 0u) r &= 0x0000FFFFu;
-  return r;
-}
 // (w ^ flip) & mask in one operation.
 template <bool ASYM>
 __device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask) {
@@ -535,6 +529,7 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
       nmf[nt] = l[nt] = make_float2(0.0f, 0.0f);
     }
     int x_run = 15;  // weights are held 2^x_run fold
+    uint32_t bad_rows = 0u;  // rows (two bits an nt) that see a value scale that is not finite: so is their output
 
     int stage = 0;
 #pragma unroll 1
@@ -656,13 +651,22 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
               if (!here || tok < s_lo[r] || tok >= s_hi[r]) s[mb][nt][half].x = kNegInf;
               if (!here || tok < s_lo[r + 1] || tok >= s_hi[r + 1]) s[mb][nt][half].y = kNegInf;
             }
-            // Scales that are not finite, seen or not, do not count here: a
-            // row that sees one has no finite output.
+            // A value scale that is not finite counts as 0, so that hidden
+            // tokens add nothing; a row that sees one is remembered.
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
               const uint32_t w = vs[mb][half][i];
-              vtop = attn::max_half2(vtop, ((w & 0x7C00u) != 0x7C00u ? w & 0xFFFFu : 0u) |
-                                               ((w & 0x7C000000u) != 0x7C000000u ? w & 0xFFFF0000u : 0u));
+              vs[mb][half][i] = ((w & 0x7C00u) != 0x7C00u ? w & 0xFFFFu : 0u) |
+                                ((w & 0x7C000000u) != 0x7C000000u ? w & 0xFFFF0000u : 0u);
+              vtop = attn::max_half2(vtop, vs[mb][half][i]);
+              const uint32_t own = lds_u16(st + C::kScaleAt + C::kScales + ((mb * 16 + half * 8 + g) * NG + i) * 2);
+              if ((own & 0x7C00u) == 0x7C00u) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (s[mb][nt][half].x != kNegInf) bad_rows |= 1u << (2 * nt);
+                  if (s[mb][nt][half].y != kNegInf) bad_rows |= 2u << (2 * nt);
+                }
+              }
             }
           }
       } else {
@@ -751,11 +755,6 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
                                              kPick[(gi & 1) * 2 + ((NG + gi) & 1)]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) pb[mb][nt][half] = mul_half2(pt[mb][nt][half], w);
-              if (edge) {  // a hidden token's weight is 0 under any scale
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  pb[mb][nt][half] = zero_where_zero(pb[mb][nt][half], pt[mb][nt][half]);
-              }
               if (ASYM) {
                 const uint32_t za = st + C::kZeroAt + C::kZeros + (mb * 16 + half * 8 + 2 * t) * NG + gi;
                 z[half] = lds_u8(za) | (lds_u8(za + NG) << 16);
@@ -789,6 +788,10 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
     cp_wait<0>();
 
     // ---- Join the warps, then store the item's result or the piece's sums.
+    if (__any_sync(0xffffffffu, bad_rows != 0u)) {
+#pragma unroll
+      for (int o2 = 4; o2 < 32; o2 <<= 1) bad_rows |= __shfl_xor_sync(0xffffffffu, bad_rows, o2);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -815,8 +818,9 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
 #pragma unroll
         for (int w = 1; w < kAttnWarps; ++w) top = fmaxf(top, s_m[w * RT + r]);
         // Codes are 2^-24 times themselves, weights 2^x_run.
-        const float scale =
+        float scale =
             (mine == top ? 1.0f : ex2(mine - top)) * __uint_as_float(static_cast<uint32_t>(127 + 24 - x_run) << 23);
+        if ((bad_rows >> (2 * nt + j)) & 1u) scale = __int_as_float(0x7FC00000);
         float* dst = buf + (warp * 8 + 2 * t + j) * C::kMergePitch + 4 * g;
 #pragma unroll
         for (int c = 0; c < DB; ++c) {

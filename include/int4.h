@@ -431,7 +431,8 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * scales, in fp16: off by at most 2^-11 of themselves, or, where they are more
  * than 2^20 below the largest, 2^-32 of that.  Deterministic for given sizes,
  * lengths and device.
- * NaN or infinity in a query makes its own rows NaN.
+ * NaN or infinity in a query makes its own rows NaN, a value scale that is not
+ * finite the outputs (not the lse) of the rows that see its token.
  *
  * `path`: INT4_PATH_AUTO takes a tensor-core kernel where one can run, else the
  * general kernel (INT4_PATH_SIMT).  INT4_PATH_DECODE, for few query rows: bf16 or
