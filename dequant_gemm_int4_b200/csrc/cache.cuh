@@ -65,10 +65,15 @@ struct AttentionArgs {
   int32_t max_pages;
   int32_t q_heads;
   int32_t ratio;  // q_heads / heads
+  uint32_t ratio_m, ratio_s;  // r / ratio = (r * ratio_m >> 32) >> ratio_s for 0 <= r < 2^31, ratio > 1
   int32_t causal;
   int32_t window;  // 0: none
   float sm_scale;
 
+  // Row r of a sequence's (query token, query head of a group) rows: its token.
+  __device__ __forceinline__ int token_of(int r) const {
+    return ratio == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), ratio_m) >> ratio_s);
+  }
   // Cached tokens of sequence b, never more than its row of the table holds.
   __device__ __forceinline__ int kv_len(int b) const {
     const int64_t cap = static_cast<int64_t>(max_pages) * cache.page_size;

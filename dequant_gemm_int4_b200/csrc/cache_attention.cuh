@@ -75,11 +75,12 @@ struct RowTile {
   int lo, hi, steps;
   __device__ __forceinline__ void set(const AttentionArgs& a, int len, int count, int rt, int RT) {
     const int step = attention_step(a.cache.head_dim, RT);
-    const int r0 = rt * RT;
-    const int r1 = min(r0 + RT, count * a.ratio) - 1;
+    const int r0 = rt * RT, rows = count * a.ratio;
+    const int r1 = min(r0 + RT, rows) - 1;
+    const int i0 = a.token_of(r0), i1 = a.token_of(r1);  // the tile's first and last query token
     int lo0, hi0, lo1, hi1;
-    a.visible(len - count + r0 / a.ratio, len, lo0, hi0);
-    a.visible(len - count + r1 / a.ratio, len, lo1, hi1);
+    a.visible(len - count + i0, len, lo0, hi0);
+    a.visible(len - count + i1, len, lo1, hi1);
     lo = lo0 & -(step / kAttnWarps);
     hi = hi1;
     steps = hi > lo ? (hi - lo + step - 1) / step : 0;
@@ -104,6 +105,69 @@ __device__ __forceinline__ int head_units(const AttentionArgs& a, int b, int RT)
   }
   return u;
 }
+
+// The units (steps, over all heads) of all sequences, counted in their order
+// by each warp for itself: lane l holds the sequences [l per, (l + 1) per).
+struct Plan {
+  int units;       // of all sequences
+  int per;
+  int mine, upto;  // of this lane's sequences; of those and all before
+
+  __device__ __forceinline__ Plan(const AttentionArgs& a, int RT) {
+    const int lane = threadIdx.x & 31;
+    per = (a.batch + 31) / 32;
+    mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const int b = lane * per + i;
+      if (b < a.batch) mine += head_units(a, b, RT) * a.cache.heads;
+    }
+    upto = scan(mine);
+    units = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  __device__ __forceinline__ static int scan(int v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    return v;
+  }
+  // The sequence that holds unit u (0 <= u < units), and u's place in it.
+  __device__ __forceinline__ void find(const AttentionArgs& a, int RT, int u, int& b, int& off) const {
+    const int lane = threadIdx.x & 31;
+    const int owner = __ffs(__ballot_sync(0xffffffffu, upto > u)) - 1;
+    int before = __shfl_sync(0xffffffffu, upto - mine, owner);
+    b = owner * per;
+    off = u - before;
+    if (per == 1) return;
+    for (int i0 = 0; i0 < per; i0 += 32) {
+      const int x = b + i0 + lane;
+      const int v = i0 + lane < per && x < a.batch ? head_units(a, x, RT) * a.cache.heads : 0;
+      const int sum = scan(v);
+      const uint32_t past = __ballot_sync(0xffffffffu, before + sum > u);
+      if (past != 0u) {
+        const int at = __ffs(past) - 1;
+        b += i0 + at;
+        off = u - before - __shfl_sync(0xffffffffu, sum - v, at);
+        return;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  // Writes prefix[b + 1], the units up to and with sequence b, for the joins.
+  __device__ __forceinline__ void store(const AttentionArgs& a, int RT, int32_t* prefix) const {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) prefix[0] = 0;
+    int sum = upto - mine;
+    for (int i = 0; i < per; ++i) {
+      const int b = lane * per + i;
+      if (b >= a.batch) break;
+      sum += per == 1 ? mine : head_units(a, b, RT) * a.cache.heads;
+      prefix[b + 1] = sum;
+    }
+  }
+};
 
 // How `units` steps are shared: the first `more` blocks take `each` + 1, the
 // other active ones `each`.
@@ -237,6 +301,13 @@ __device__ __forceinline__ float2 lds_f2(uint32_t a) {
   return v;
 }
 
+// Four 16-bit elements, as one load where they are 8-byte aligned.
+__device__ __forceinline__ uint2 load_four(const uint16_t* p, bool aligned) {
+  if (aligned) return __ldg(reinterpret_cast<const uint2*>(p));
+  return make_uint2(__ldg(p) | (static_cast<uint32_t>(__ldg(p + 1)) << 16),
+                    __ldg(p + 2) | (static_cast<uint32_t>(__ldg(p + 3)) << 16));
+}
+
 // 16-byte chunk c of token row r in a tile: permuted so that the 8 rows of
 // an ldmatrix fall into different banks.
 template <int RB>
@@ -269,76 +340,20 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
   int* const s_hi = s_lo + RT;                                  // [RT]
   float* const s_m = reinterpret_cast<float*>(s_hi + RT);       // [warps][RT]
   float* const s_l = s_m + kAttnWarps * RT;                     // [warps][RT]
-  __shared__ int s_scan[kAttnWarps];
-  __shared__ int s_off, s_b;
 
-  // ---- This block's share: units [u0, u1) of all, beginning in sequence b.
-  int units = 0, mine = 0, upto = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kAttnThreads) {
-    const int b = b0 + tid;
-    mine = b < a.batch ? head_units(a, b, RT) * cache.heads : 0;
-    upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    if (lane == 31) s_scan[warp] = upto;
-    __syncthreads();
-    int all = 0;
-    for (int w = 0; w < kAttnWarps; ++w) {
-      if (w < warp) upto += s_scan[w];
-      all += s_scan[w];
-    }
-    upto += units;  // inclusive, over all sequences up to b
-    if (blockIdx.x == 0 && b < a.batch) ws.prefix[b + 1] = upto;
-    units += all;
-    __syncthreads();
-  }
-  if (blockIdx.x == 0 && tid == 0) ws.prefix[0] = 0;
+  // ---- This block's share: units [u0, u0 + left) of all.
+  const Plan plan(a, RT);
+  if (blockIdx.x == 0 && warp == 0) plan.store(a, RT, ws.prefix);
   // The join may be set up now; it waits for this grid's end before it reads.
   ptx::launch_dependents();
-  const Shares shares(units, ws.blocks);
+  const Shares shares(plan.units, ws.blocks);
   if (static_cast<int>(blockIdx.x) >= shares.active) return;
   const int u0 = shares.begin(blockIdx.x);
   int left = shares.begin(blockIdx.x + 1) - u0;
-  if (a.batch <= kAttnThreads) {
-    if (upto - mine <= u0 && u0 < upto) {
-      s_b = tid;
-      s_off = u0 - (upto - mine);
-    }
-  } else {
-    int before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kAttnThreads) {
-      const int b = b0 + tid;
-      mine = b < a.batch ? head_units(a, b, RT) * cache.heads : 0;
-      upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      if (lane == 31) s_scan[warp] = upto;
-      __syncthreads();
-      int all = 0;
-      for (int w = 0; w < kAttnWarps; ++w) {
-        if (w < warp) upto += s_scan[w];
-        all += s_scan[w];
-      }
-      upto += before;
-      if (upto - mine <= u0 && u0 < upto) {
-        s_b = b;
-        s_off = u0 - (upto - mine);
-      }
-      before += all;
-      __syncthreads();
-      if (before > u0) break;  // the same for every thread
-    }
-  }
-  __syncthreads();
 
   // ---- The item in which the share begins.
-  int b = s_b;
+  int b, off;
+  plan.find(a, RT, u0, b, off);
   int first, count;
   a.queries(b, first, count);
   int len = a.kv_len(b);
@@ -347,7 +362,6 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
   RowTile tile;
   {
     const int per_head = head_units(a, b, RT);
-    int off = s_off;
     h = off / per_head;
     off -= h * per_head;
     tile.set(a, len, count, 0, RT);
@@ -360,6 +374,7 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
 
   // q takes the sign of sm_scale.
   const float sign = a.sm_scale > 0.0f ? 1.0f : (a.sm_scale < 0.0f ? -1.0f : 0.0f);
+  const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 7) == 0 && a.q_token_stride % 4 == 0 && a.q_head_stride % 4 == 0;
   const int split = max(0, (TOK == 64 ? 6 : 5) - page_shift);
   const uint32_t ring = ptx::smem_u32(smem) + warp * C::kStages * C::kStage;
 
@@ -448,42 +463,64 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
     for (int k = 0; k < C::kStages - 1; ++k) issue(k, k);
 
     // ---- Queries of the tile: fp16 in fragment order, group sums, bounds.
-    for (int r = warp; r < RT; r += kAttnWarps) {
-      float v[DB];
+    // Eight lanes a row, lane j of them with elements 4 j .. 4 j + 3 of each
+    // block of 32.
+#pragma unroll
+    for (int rr = 0; rr < RT; rr += 4 * kAttnWarps) {
+      if (rr + warp * 4 >= RT) break;
+      const int r = rr + warp * 4 + (lane >> 3), j = lane & 7;
       const bool live = r < rows;
-      const int i = live ? (r0 + r) / a.ratio : 0;
+      const int i = live ? a.token_of(r0 + r) : 0;
       const int hq = h * a.ratio + (live ? r0 + r - i * a.ratio : 0);
-      const T* qp = static_cast<const T*>(a.q) + (first + i) * a.q_token_stride + hq * a.q_head_stride;
-      float top = 0.0f;
+      const T* qp = static_cast<const T*>(a.q) + (first + i) * a.q_token_stride + hq * a.q_head_stride + 4 * j;
+      uint2 raw[DB];
 #pragma unroll
       for (int c = 0; c < DB; ++c) {
-        v[c] = live ? Elem<T>::load(qp + 32 * c + lane) : 0.0f;
-        top = fmaxf(top, fabsf(v[c]));
+        raw[c] = make_uint2(0u, 0u);
+        if (live) raw[c] = load_four(reinterpret_cast<const uint16_t*>(qp + 32 * c), q_vec);
       }
+      auto lo_of = [](uint32_t x) {
+        return std::is_same<T, __half>::value ? f16_bits_to_float(x & 0xFFFFu) : __uint_as_float(x << 16);
+      };
+      auto hi_of = [](uint32_t x) {
+        return std::is_same<T, __half>::value ? f16_bits_to_float(x >> 16) : __uint_as_float(x & 0xFFFF0000u);
+      };
+      float top = 0.0f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int c = 0; c < DB; ++c)
+        top = fmaxf(top, fmaxf(fmaxf(fabsf(lo_of(raw[c].x)), fabsf(hi_of(raw[c].x))),
+                               fmaxf(fabsf(lo_of(raw[c].y)), fabsf(hi_of(raw[c].y)))));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       // top in [2^e, 2^(e+1)); elements are scaled by 2^(14 - e).
       int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
       e = e < -100 ? -100 : e;
       const float scale = sign * __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-      const int nt = r >> 3, gr = r & 7, tl = lane >> 3, el = lane & 7;
+      // Elements 8 t + 2 s + k and 8 t + 2 s + k + 4 of a block are the two
+      // halves of B register k of step s and lane t of the row's quad: lanes
+      // 2 t and 2 t + 1 here hold the two, and store a step each.  k = 1
+      // divided by 16.
+      const int nt = r >> 3, gr = r & 7, odd = j & 1;
       float sum = 0.0f;
 #pragma unroll
       for (int c = 0; c < DB; ++c) {
-        const __half x = __float2half_rn(v[c] * scale);
-        const __half y = (el & 1) ? __hmul(x, __float2half_rn(0.0625f)) : x;
-        const int step = (el >> 1) & 1, reg = el & 1, half = el >> 2;
-        const int at = ((((c * 2 + step) * NT + nt) * 32 + gr * 4 + tl) * 2 + reg) * 2 + half;
-        reinterpret_cast<__half*>(sq)[at] = y;
-        sum += __half2float(x);
+        const uint32_t x01 = pack_half2(lo_of(raw[c].x) * scale, hi_of(raw[c].x) * scale);
+        const uint32_t x23 = pack_half2(lo_of(raw[c].y) * scale, hi_of(raw[c].y) * scale);
+        sum += (f16_bits_to_float(x01 & 0xFFFFu) + f16_bits_to_float(x01 >> 16)) +
+               (f16_bits_to_float(x23 & 0xFFFFu) + f16_bits_to_float(x23 >> 16));
+        const uint32_t y01 = mul_half2(x01, 0x2C003C00u), y23 = mul_half2(x23, 0x2C003C00u);
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? y01 : y23, 1);
+        const uint32_t low = odd ? got : y01, high = odd ? y23 : got;
+        reinterpret_cast<uint2*>(sq)[((c * 2 + odd) * NT + nt) * 32 + gr * 4 + (j >> 1)] =
+            make_uint2(__byte_perm(low, high, 0x5410), __byte_perm(low, high, 0x7632));
         if (c % C::BPG == C::BPG - 1) {
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (lane == 0) s_qsum[(c / C::BPG) * RT + r] = -sum * (ASYM ? 0x1p-24f : 0x1p-21f);
+          for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (j == 0) s_qsum[(c / C::BPG) * RT + r] = -sum * (ASYM ? 0x1p-24f : 0x1p-21f);
           sum = 0.0f;
         }
       }
-      if (lane == 0) {
+      if (j == 0) {
         int lo = 0, hi = 0;
         if (live) a.visible(len - count + i, len, lo, hi);
         s_lo[r] = lo;
@@ -834,6 +871,7 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
         }
       }
       __syncthreads();
+#pragma unroll 1
       for (int k = tid; k < 8 * (D / 4); k += kAttnThreads) {
         const int rr = k / (D / 4), d = (k % (D / 4)) * 4;
         const int r = nt * 8 + rr;
@@ -853,7 +891,7 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
           sum += s_l[w * RT + r] * (mw == top ? 1.0f : ex2(mw - top));
         }
         if (whole) {
-          const int i = (r0 + r) / a.ratio;
+          const int i = a.token_of(r0 + r);
           const int at = (first + i) * a.q_heads + h * a.ratio + (r0 + r - i * a.ratio);
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
           T* out = static_cast<T*>(a.out) + static_cast<int64_t>(at) * D + d;
@@ -939,37 +977,55 @@ __global__ void __launch_bounds__(256)
   }
   const bool join = p_end - p0 > 1;
   const bool empty = b >= 0 && steps == 0;
+  const int rr = r - rt * RT;
+  // The first piece ends its block's share, every other one begins its own.
+  auto slot = [&](int p) { return static_cast<int64_t>(2 * p + (p == p0 ? 1 : 0)) * RT + rr; };
   float4 v[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   float top = kNegInf, sum = 0.0f;
-  const int rr = r - rt * RT;
   if (join) {
-    // The first piece ends its block's share, every other one begins its own.
-    auto slot = [&](int p) { return (2 * p + (p == p0 ? 1 : 0)) * RT + rr; };
     for (int p = p0 + lane; p < p_end; p += 32) top = fmaxf(top, ws.ml[slot(p) * 2]);
+    // This warp's pieces, four at a time (the first four beside the maxima).
+    float4 x[4][2];
+    float mp[4];
+    auto load = [&](int p) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int q = p + k * wpr;
+        mp[k] = kNegInf;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int d = i * 128 + lane * 4;
+          x[k][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (q < p_end && d < D) x[k][i] = *reinterpret_cast<const float4*>(ws.o + slot(q) * D + d);
+        }
+        if (q < p_end) mp[k] = ws.ml[slot(q) * 2];
+      }
+    };
+    int p = p0 + warp % wpr;
+    load(p);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int p = p0 + lane; p < p_end; p += 32) {
-      const float mp = ws.ml[slot(p) * 2];
-      sum += ws.ml[slot(p) * 2 + 1] * (mp == top ? 1.0f : attn::ex2(mp - top));
+    for (int q = p0 + lane; q < p_end; q += 32) {
+      const float mq = ws.ml[slot(q) * 2];
+      sum += ws.ml[slot(q) * 2 + 1] * (mq == top ? 1.0f : attn::ex2(mq - top));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll 4
-    for (int p = p0 + warp % wpr; p < p_end; p += wpr) {
-      const int64_t s = slot(p);
-      const float mp = ws.ml[s * 2];
-      const float w = mp == top ? 1.0f : attn::ex2(mp - top);
+    while (p < p_end) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int d = i * 128 + lane * 4;
-        if (d < D) {
-          const float4 x = *reinterpret_cast<const float4*>(ws.o + s * D + d);
-          v[i].x = fmaf(w, x.x, v[i].x);
-          v[i].y = fmaf(w, x.y, v[i].y);
-          v[i].z = fmaf(w, x.z, v[i].z);
-          v[i].w = fmaf(w, x.w, v[i].w);
+      for (int k = 0; k < 4; ++k) {
+        if (p + k * wpr >= p_end) break;
+        const float w = mp[k] == top ? 1.0f : attn::ex2(mp[k] - top);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          v[i].x = fmaf(w, x[k][i].x, v[i].x);
+          v[i].y = fmaf(w, x[k][i].y, v[i].y);
+          v[i].z = fmaf(w, x[k][i].z, v[i].z);
+          v[i].w = fmaf(w, x[k][i].w, v[i].w);
         }
       }
+      p += 4 * wpr;
+      if (p < p_end) load(p);
     }
   }
   if (wpr > 1) {  // one row a block: join is the same for all its threads
@@ -1039,7 +1095,7 @@ __global__ void __launch_bounds__(256)
       tile.set(a, len, count, rt, RT);
       const int r = rt * RT + rr;
       if (tile.steps > 0 || r >= count * a.ratio) continue;
-      const int i = r / a.ratio;
+      const int i = a.token_of(r);
       for (int h = 0; h < a.cache.heads; ++h) {
         const int at = (first + i) * a.q_heads + h * a.ratio + r - i * a.ratio;
         for (int d = lane * 4; d < D; d += 128) store(at, d, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
@@ -1058,6 +1114,7 @@ __global__ void __launch_bounds__(256)
     const int mid = (b + hi_b) >> 1;
     if (ws.prefix[mid] <= last) b = mid; else hi_b = mid;
   }
+  const int in_seq = last - ws.prefix[b];
   int first, count;
   a.queries(b, first, count);
   const int len = a.kv_len(b), n = row_tiles(a, count, RT);
@@ -1069,7 +1126,6 @@ __global__ void __launch_bounds__(256)
     per_head += tile.steps;
   }
   per_head = __reduce_add_sync(0xffffffffu, per_head);
-  const int in_seq = last - ws.prefix[b];
   const int h = in_seq / per_head, off = in_seq - h * per_head;
   int rt = 0, before = 0, steps = 0;
   for (int i0 = 0, sum = 0; i0 < n; i0 += 32) {
@@ -1092,7 +1148,7 @@ __global__ void __launch_bounds__(256)
     }
     sum += __shfl_sync(0xffffffffu, upto, 31);
   }
-  const int item = ws.prefix[b] + h * per_head + before;
+  const int item = last - off + before;
   if (item < begin || item + steps <= last + 1) return;  // begun earlier, or ends here
   const int p_end = shares.block_of(item + steps - 1) + 1;
   const int r = rt * RT + rr;
@@ -1118,7 +1174,7 @@ __global__ void __launch_bounds__(256)
       }
     }
   }
-  const int i = r / a.ratio;
+  const int i = a.token_of(r);
   const int at = (first + i) * a.q_heads + h * a.ratio + r - i * a.ratio;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll

@@ -199,10 +199,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                                                    ~static_cast<uintptr_t>(1023));
   const CacheView& cache = a.cache;
   Bars* const bars = reinterpret_cast<Bars*>(smem + L::offBar);
-  uint32_t* const misc = reinterpret_cast<uint32_t*>(smem + L::offMisc);  // TMEM address, abort flag, plan
+  uint32_t* const misc = reinterpret_cast<uint32_t*>(smem + L::offMisc);  // TMEM address, abort flag, s_steps
   volatile uint32_t* const abort_flag = misc + 1;
-  int* const s_plan = reinterpret_cast<int*>(misc + 2);  // sequence, offset; then scan[4]
-  volatile int* const s_steps = reinterpret_cast<volatile int*>(misc + 8);  // [2]: tiles of an item, 0 after the last
+  volatile int* const s_steps = reinterpret_cast<volatile int*>(misc + 2);  // [2]: tiles of an item, 0 after the last
   float* const s_scale = reinterpret_cast<float*>(smem + L::offScale);
   Bits* const s_bits = reinterpret_cast<Bits*>(smem + L::offBits);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -233,68 +232,15 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     ptx::tmem_relinquish();
   }
 
-  // ---- This block's share (as in attention_mma_kernel; the first 128 threads).
-  int units = 0;
-  {
-    int mine = 0, upto = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 128) {
-      const int b = b0 + tid;
-      if (tid < 128) {
-        mine = b < a.batch ? head_units(a, b, kRows) * cache.heads : 0;
-        upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += v;
-        }
-        if (lane == 31) s_plan[2 + warp] = upto;
-      }
-      __syncthreads();
-      int all = 0;
-      for (int w = 0; w < 4; ++w) {
-        if (w < warp) upto += s_plan[2 + w];
-        all += s_plan[2 + w];
-      }
-      if (blockIdx.x == 0 && tid < 128 && b < a.batch) ws.prefix[b + 1] = units + upto;
-      units += all;
-      __syncthreads();
-    }
-    if (blockIdx.x == 0 && tid == 0) ws.prefix[0] = 0;
-  }
-  const Shares shares(units, ws.blocks);
+  // ---- This block's share (each warp finds it).
+  const Plan plan(a, kRows);
+  if (blockIdx.x == 0 && warp == 2) plan.store(a, kRows, ws.prefix);
+  const Shares shares(plan.units, ws.blocks);
   const bool working = static_cast<int>(blockIdx.x) < shares.active;
   const int u0 = working ? shares.begin(blockIdx.x) : 0;
   const int my_units = working ? shares.begin(blockIdx.x + 1) - u0 : 0;
-  if (working) {
-    int before = 0;
-    for (int b0 = 0; b0 < a.batch && before <= u0; b0 += 128) {  // the same for every thread
-      const int b = b0 + tid;
-      int mine = 0, upto = 0;
-      if (tid < 128) {
-        mine = b < a.batch ? head_units(a, b, kRows) * cache.heads : 0;
-        upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += v;
-        }
-        if (lane == 31) s_plan[2 + warp] = upto;
-      }
-      __syncthreads();
-      int all = 0;
-      for (int w = 0; w < 4; ++w) {
-        if (w < warp) upto += s_plan[2 + w];
-        all += s_plan[2 + w];
-      }
-      upto += before;
-      if (tid < 128 && upto - mine <= u0 && u0 < upto) {
-        s_plan[0] = b;
-        s_plan[1] = u0 - (upto - mine);
-      }
-      before += all;
-      __syncthreads();
-    }
-  }
+  int b_start = 0, off_start = 0;
+  if (working) plan.find(a, kRows, u0, b_start, off_start);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -349,7 +295,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   Walk& w = s_walk[warp];
   auto walk_start = [&]() {
     Walk x;
-    x.start(a, s_plan[0], s_plan[1], my_units);
+    x.start(a, b_start, off_start, my_units);
     if (lane == 0) w = x;
     __syncwarp();
   };
@@ -561,7 +507,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       float f;
       int lo = 0, hi = 0;
       {
-        const int i_tok = (r0 + (live_row ? r : 0)) / a.ratio;
+        const int i_tok = a.token_of(r0 + (live_row ? r : 0));
         const int hq = w.h * a.ratio + (r0 + (live_row ? r : 0)) - i_tok * a.ratio;
         uint32_t raw[D / 2];
         const T* qp = static_cast<const T*>(a.q) + (w.first + i_tok) * a.q_token_stride + hq * a.q_head_stride;
@@ -775,7 +721,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       ptx::tc_fence_after();
       const bool whole = n == w.tile.steps;
       const float sum = l.x + l.y;
-      const int i_tok = (r0 + (live_row ? r : 0)) / a.ratio;
+      const int i_tok = a.token_of(r0 + (live_row ? r : 0));
       const int at = (w.first + i_tok) * a.q_heads + w.h * a.ratio + (r0 + (live_row ? r : 0)) - i_tok * a.ratio;
       const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (w.s0 == 0 ? 1 : 0)) * kRows + r;
       const float back = __uint_as_float(static_cast<uint32_t>(127 - x_run) << 23);

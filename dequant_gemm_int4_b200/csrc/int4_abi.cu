@@ -526,9 +526,19 @@ int int4_cache_attention(const int4_cache* cache, const void* q, int64_t q_token
                   need, workspace_bytes);
     return int4lib::fail(INT4_ERR_ARG, msg);
   }
+  // Division by the ratio for operands below 2^31: m = ceil(2^(31 + b) / ratio)
+  // with 2^(b - 1) < ratio <= 2^b.
+  uint32_t ratio_m = 0, ratio_s = 0;
+  const uint32_t ratio = static_cast<uint32_t>(q_heads / view.heads);
+  if (ratio > 1) {
+    uint32_t b = 1;
+    while ((1ull << b) < ratio) ++b;
+    ratio_m = static_cast<uint32_t>(((1ull << (31 + b)) + ratio - 1) / ratio);
+    ratio_s = b - 1;
+  }
   const int4lib::AttentionArgs a = {view, q, q_token_stride, q_head_stride, out, lse, page_table,
                                     table_stride, kv_lens, q_starts, static_cast<int32_t>(rows), batch, max_pages, q_heads,
-                                    q_heads / view.heads, causal != 0 ? 1 : 0, window, sm_scale};
+                                    q_heads / view.heads, ratio_m, ratio_s, causal != 0 ? 1 : 0, window, sm_scale};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = path == INT4_PATH_SIMT     ? int4lib::launch_cache_attention_any(a, t, s)
                         : path == INT4_PATH_DECODE ? int4lib::launch_cache_attention_mma(a, t, workspace, s)
