@@ -141,6 +141,13 @@ struct Plan {
     b = owner * per;
     off = u - before;
     if (per == 1) return;
+    if (per <= 8) {  // one after the other, the same in every lane
+      for (;; ++b) {
+        const int v = head_units(a, b, RT) * a.cache.heads;
+        if (off < v) return;
+        off -= v;
+      }
+    }
     for (int i0 = 0; i0 < per; i0 += 32) {
       const int x = b + i0 + lane;
       const int v = i0 + lane < per && x < a.batch ? head_units(a, x, RT) * a.cache.heads : 0;
@@ -983,49 +990,53 @@ __global__ void __launch_bounds__(256)
   float4 v[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   float top = kNegInf, sum = 0.0f;
   if (join) {
-    for (int p = p0 + lane; p < p_end; p += 32) top = fmaxf(top, ws.ml[slot(p) * 2]);
-    // This warp's pieces, four at a time (the first four beside the maxima).
-    float4 x[4][2];
-    float mp[4];
-    auto load = [&](int p) {
+    const int pieces = p_end - p0;
+    for (int base = 0; base < pieces; base += 32) {
+      // A lane's piece of these 32, and the first four of the warp's own.
+      const int here = min(pieces - base, 32);
+      float2 ml = make_float2(kNegInf, 0.0f);
+      if (lane < here) ml = *reinterpret_cast<const float2*>(ws.ml + slot(p0 + base + lane) * 2);
+      float4 x[4][2];
+      auto load = [&](int k0) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int q = p + k * wpr;
-        mp[k] = kNegInf;
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int d = i * 128 + lane * 4;
-          x[k][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (q < p_end && d < D) x[k][i] = *reinterpret_cast<const float4*>(ws.o + slot(q) * D + d);
-        }
-        if (q < p_end) mp[k] = ws.ml[slot(q) * 2];
+          for (int i = 0; i < 2; ++i) {
+            const int d = i * 128 + lane * 4, q = k0 + k * wpr;
+            x[k][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (q < here && d < D) x[k][i] = *reinterpret_cast<const float4*>(ws.o + slot(p0 + base + q) * D + d);
+          }
+      };
+      load(warp % wpr);
+      float m = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = fmaxf(m, top);
+      const float old = top == m ? 1.0f : attn::ex2(top - m);
+      const float w = ml.x == m ? 1.0f : attn::ex2(ml.x - m);
+      float l = ml.y * w;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      top = m;
+      sum = fmaf(sum, old, l);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v[i].x *= old; v[i].y *= old; v[i].z *= old; v[i].w *= old;
       }
-    };
-    int p = p0 + warp % wpr;
-    load(p);
+      for (int k0 = warp % wpr; k0 < here; k0 += 4 * wpr) {
+        if (k0 >= 4 * wpr) load(k0);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int q = p0 + lane; q < p_end; q += 32) {
-      const float mq = ws.ml[slot(q) * 2];
-      sum += ws.ml[slot(q) * 2 + 1] * (mq == top ? 1.0f : attn::ex2(mq - top));
-    }
+        for (int k = 0; k < 4; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, (k0 + k * wpr) & 31);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    while (p < p_end) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (p + k * wpr >= p_end) break;
-        const float w = mp[k] == top ? 1.0f : attn::ex2(mp[k] - top);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          v[i].x = fmaf(w, x[k][i].x, v[i].x);
-          v[i].y = fmaf(w, x[k][i].y, v[i].y);
-          v[i].z = fmaf(w, x[k][i].z, v[i].z);
-          v[i].w = fmaf(w, x[k][i].w, v[i].w);
+          for (int i = 0; i < 2; ++i) {  // what is not there is 0
+            v[i].x = fmaf(wk, x[k][i].x, v[i].x);
+            v[i].y = fmaf(wk, x[k][i].y, v[i].y);
+            v[i].z = fmaf(wk, x[k][i].z, v[i].z);
+            v[i].w = fmaf(wk, x[k][i].w, v[i].w);
+          }
         }
       }
-      p += 4 * wpr;
-      if (p < p_end) load(p);
     }
   }
   if (wpr > 1) {  // one row a block: join is the same for all its threads
