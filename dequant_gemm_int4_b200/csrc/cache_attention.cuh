@@ -465,95 +465,9 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
       }
       cp_commit();
     };
-    // The first tiles are on their way while the queries are laid out.
-#pragma unroll 1
-    for (int k = 0; k < C::kStages - 1; ++k) issue(k, k);
-
-    // ---- Queries of the tile: fp16 in fragment order, group sums, bounds.
-    // Eight lanes a row, lane j of them with elements 4 j .. 4 j + 3 of each
-    // block of 32.
-#pragma unroll
-    for (int rr = 0; rr < RT; rr += 4 * kAttnWarps) {
-      if (rr + warp * 4 >= RT) break;
-      const int r = rr + warp * 4 + (lane >> 3), j = lane & 7;
-      const bool live = r < rows;
-      const int i = live ? a.token_of(r0 + r) : 0;
-      const int hq = h * a.ratio + (live ? r0 + r - i * a.ratio : 0);
-      const T* qp = static_cast<const T*>(a.q) + (first + i) * a.q_token_stride + hq * a.q_head_stride + 4 * j;
-      uint2 raw[DB];
-#pragma unroll
-      for (int c = 0; c < DB; ++c) {
-        raw[c] = make_uint2(0u, 0u);
-        if (live) raw[c] = load_four(reinterpret_cast<const uint16_t*>(qp + 32 * c), q_vec);
-      }
-      auto lo_of = [](uint32_t x) {
-        return std::is_same<T, __half>::value ? f16_bits_to_float(x & 0xFFFFu) : __uint_as_float(x << 16);
-      };
-      auto hi_of = [](uint32_t x) {
-        return std::is_same<T, __half>::value ? f16_bits_to_float(x >> 16) : __uint_as_float(x & 0xFFFF0000u);
-      };
-      float top = 0.0f;
-#pragma unroll
-      for (int c = 0; c < DB; ++c)
-        top = fmaxf(top, fmaxf(fmaxf(fabsf(lo_of(raw[c].x)), fabsf(hi_of(raw[c].x))),
-                               fmaxf(fabsf(lo_of(raw[c].y)), fabsf(hi_of(raw[c].y)))));
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // top in [2^e, 2^(e+1)); elements are scaled by 2^(14 - e).
-      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-      e = e < -100 ? -100 : e;
-      const float scale = sign * __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-      // Elements 8 t + 2 s + k and 8 t + 2 s + k + 4 of a block are the two
-      // halves of B register k of step s and lane t of the row's quad: lanes
-      // 2 t and 2 t + 1 here hold the two, and store a step each.  k = 1
-      // divided by 16.
-      const int nt = r >> 3, gr = r & 7, odd = j & 1;
-      float sum = 0.0f;
-#pragma unroll
-      for (int c = 0; c < DB; ++c) {
-        const uint32_t x01 = pack_half2(lo_of(raw[c].x) * scale, hi_of(raw[c].x) * scale);
-        const uint32_t x23 = pack_half2(lo_of(raw[c].y) * scale, hi_of(raw[c].y) * scale);
-        sum += (f16_bits_to_float(x01 & 0xFFFFu) + f16_bits_to_float(x01 >> 16)) +
-               (f16_bits_to_float(x23 & 0xFFFFu) + f16_bits_to_float(x23 >> 16));
-        const uint32_t y01 = mul_half2(x01, 0x2C003C00u), y23 = mul_half2(x23, 0x2C003C00u);
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? y01 : y23, 1);
-        const uint32_t low = odd ? got : y01, high = odd ? y23 : got;
-        reinterpret_cast<uint2*>(sq)[((c * 2 + odd) * NT + nt) * 32 + gr * 4 + (j >> 1)] =
-            make_uint2(__byte_perm(low, high, 0x5410), __byte_perm(low, high, 0x7632));
-        if (c % C::BPG == C::BPG - 1) {
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (j == 0) s_qsum[(c / C::BPG) * RT + r] = -sum * (ASYM ? 0x1p-24f : 0x1p-21f);
-          sum = 0.0f;
-        }
-      }
-      if (j == 0) {
-        int lo = 0, hi = 0;
-        if (live) a.visible(len - count + i, len, lo, hi);
-        s_lo[r] = lo;
-        s_hi[r] = hi;
-        // Positive, so that it may be applied after the maximum.
-        const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23) * (fabsf(a.sm_scale) * 1.4426950408889634f);
-        s_f[r] = sign == 0.0f ? 1.0f : fminf(fmaxf(f1, 0x1p-126f), 0x1p127f);
-      }
-    }
-    __syncthreads();
-    // Tokens that every row of the tile sees.
-    const int all_lo = s_lo[rows - 1], all_hi = s_hi[0];
-
+    int all_lo = 0, all_hi = 0;  // tokens that every row of the tile sees
     uint2 qf[C::kQInRegs ? DB * 2 * NT : 1];
-    if (C::kQInRegs) {
-#pragma unroll
-      for (int i = 0; i < DB * 2 * NT; ++i) qf[i] = reinterpret_cast<const uint2*>(sq)[i * 32 + lane];
-    }
-    float2 f[NT];
-    float2 qs1[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      f[nt] = *reinterpret_cast<const float2*>(s_f + nt * 8 + 2 * t);
-      qs1[nt] = *reinterpret_cast<const float2*>(s_qsum + nt * 8 + 2 * t);
-    }
-
+    float2 f[NT], qs1[NT];
     float o[DB][2][NT][4], zo[NG][NT][4];
     // Per row: the maximum of S / f, -maximum * f (0 before the first token),
     // and this lane's part of the sum.
@@ -575,12 +489,98 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
     int x_run = 15;  // weights are held 2^x_run fold
     uint32_t bad_rows = 0u;  // rows (two bits an nt) that see a value scale that is not finite: so is their output
 
-    int stage = 0;
+    int stage = 0, fill = 0;  // the tile in use, the one to be filled
 #pragma unroll 1
-    for (int k = 0; k < n; ++k) {
-      cp_wait<C::kStages - 2>();
-      __syncwarp();
-      issue(k + C::kStages - 1, stage == 0 ? C::kStages - 1 : stage - 1);
+    for (int k = 1 - C::kStages; k < n; ++k) {
+      if (k == 0) {  // the first tiles are on their way: the queries now
+        // ---- Queries of the tile: fp16 in fragment order, group sums, bounds.
+        // Eight lanes a row, lane j of them with elements 4 j .. 4 j + 3 of each
+        // block of 32.
+#pragma unroll
+        for (int rr = 0; rr < RT; rr += 4 * kAttnWarps) {
+          if (rr + warp * 4 >= RT) break;
+          const int r = rr + warp * 4 + (lane >> 3), j = lane & 7;
+          const bool live = r < rows;
+          const int i = live ? a.token_of(r0 + r) : 0;
+          const int hq = h * a.ratio + (live ? r0 + r - i * a.ratio : 0);
+          const T* qp = static_cast<const T*>(a.q) + (first + i) * a.q_token_stride + hq * a.q_head_stride + 4 * j;
+          uint2 raw[DB];
+#pragma unroll
+          for (int c = 0; c < DB; ++c) {
+            raw[c] = make_uint2(0u, 0u);
+            if (live) raw[c] = load_four(reinterpret_cast<const uint16_t*>(qp + 32 * c), q_vec);
+          }
+          auto lo_of = [](uint32_t x) {
+            return std::is_same<T, __half>::value ? f16_bits_to_float(x & 0xFFFFu) : __uint_as_float(x << 16);
+          };
+          auto hi_of = [](uint32_t x) {
+            return std::is_same<T, __half>::value ? f16_bits_to_float(x >> 16) : __uint_as_float(x & 0xFFFF0000u);
+          };
+          float top = 0.0f;
+#pragma unroll
+          for (int c = 0; c < DB; ++c)
+            top = fmaxf(top, fmaxf(fmaxf(fabsf(lo_of(raw[c].x)), fabsf(hi_of(raw[c].x))),
+                                   fmaxf(fabsf(lo_of(raw[c].y)), fabsf(hi_of(raw[c].y)))));
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // top in [2^e, 2^(e+1)); elements are scaled by 2^(14 - e).
+          int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+          e = e < -100 ? -100 : e;
+          const float scale = sign * __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+          // Elements 8 t + 2 s + k and 8 t + 2 s + k + 4 of a block are the two
+          // halves of B register k of step s and lane t of the row's quad: lanes
+          // 2 t and 2 t + 1 here hold the two, and store a step each.  k = 1
+          // divided by 16.
+          const int nt = r >> 3, gr = r & 7, odd = j & 1;
+          float sum = 0.0f;
+#pragma unroll
+          for (int c = 0; c < DB; ++c) {
+            const uint32_t x01 = pack_half2(lo_of(raw[c].x) * scale, hi_of(raw[c].x) * scale);
+            const uint32_t x23 = pack_half2(lo_of(raw[c].y) * scale, hi_of(raw[c].y) * scale);
+            sum += (f16_bits_to_float(x01 & 0xFFFFu) + f16_bits_to_float(x01 >> 16)) +
+                   (f16_bits_to_float(x23 & 0xFFFFu) + f16_bits_to_float(x23 >> 16));
+            const uint32_t y01 = mul_half2(x01, 0x2C003C00u), y23 = mul_half2(x23, 0x2C003C00u);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? y01 : y23, 1);
+            const uint32_t low = odd ? got : y01, high = odd ? y23 : got;
+            reinterpret_cast<uint2*>(sq)[((c * 2 + odd) * NT + nt) * 32 + gr * 4 + (j >> 1)] =
+                make_uint2(__byte_perm(low, high, 0x5410), __byte_perm(low, high, 0x7632));
+            if (c % C::BPG == C::BPG - 1) {
+#pragma unroll
+              for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+              if (j == 0) s_qsum[(c / C::BPG) * RT + r] = -sum * (ASYM ? 0x1p-24f : 0x1p-21f);
+              sum = 0.0f;
+            }
+          }
+          if (j == 0) {
+            int lo = 0, hi = 0;
+            if (live) a.visible(len - count + i, len, lo, hi);
+            s_lo[r] = lo;
+            s_hi[r] = hi;
+            // Positive, so that it may be applied after the maximum.
+            const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23) * (fabsf(a.sm_scale) * 1.4426950408889634f);
+            s_f[r] = sign == 0.0f ? 1.0f : fminf(fmaxf(f1, 0x1p-126f), 0x1p127f);
+          }
+        }
+        __syncthreads();
+        all_lo = s_lo[rows - 1];
+        all_hi = s_hi[0];
+        if (C::kQInRegs) {
+#pragma unroll
+          for (int i = 0; i < DB * 2 * NT; ++i) qf[i] = reinterpret_cast<const uint2*>(sq)[i * 32 + lane];
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          f[nt] = *reinterpret_cast<const float2*>(s_f + nt * 8 + 2 * t);
+          qs1[nt] = *reinterpret_cast<const float2*>(s_qsum + nt * 8 + 2 * t);
+        }
+      }
+      if (k >= 0) {
+        cp_wait<C::kStages - 2>();
+        __syncwarp();
+      }
+      issue(k + C::kStages - 1, fill);
+      fill = fill == C::kStages - 1 ? 0 : fill + 1;
+      if (k < 0) continue;
       const uint32_t st = ring + stage * C::kStage;
       const uint32_t live = (live_blocks >> (MB * stage)) & ((1u << MB) - 1);
       stage = stage == C::kStages - 1 ? 0 : stage + 1;
