@@ -13,6 +13,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -149,6 +150,12 @@ struct Place {
   }
 };
 
+// A new dense tensor on the cache's device (at::empty's work without its way
+// through the dispatcher, which took longer than the rest of a call's checks).
+Tensor empty(at::IntArrayRef shape, at::ScalarType type, c10::DeviceIndex device) {
+  return Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, device), std::nullopt));
+}
+
 // Device memory for one call, ordered on its stream.
 struct Scratch {
   void* p = nullptr;
@@ -225,7 +232,7 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Place place(cache.device);
     for (int i = 0; i < 2; ++i) {
       if (a[7 + i] == Py_None) {
-        out[i] = at::empty(shape, slots.options().dtype(type));
+        out[i] = empty(shape, type, cache.device);
         continue;
       }
       out[i] = tensor(a[7 + i], "out");
@@ -316,7 +323,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Place place(cache.device);
     Tensor out, lse;
     if (a[12] == Py_None) {
-      out = at::empty(q.sizes(), q.options());
+      out = empty(q.sizes(), q.scalar_type(), cache.device);
     } else {
       out = tensor(a[12], "out");
       if (out.scalar_type() != q.scalar_type() || out.sizes() != q.sizes())
@@ -331,7 +338,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       need_dense(lse, "lse");
       cache.on(lse, "lse");
     } else if (return_lse) {
-      lse = at::empty(q.sizes().slice(0, 2), q.options().dtype(at::kFloat));
+      lse = empty(q.sizes().slice(0, 2), at::kFloat, cache.device);
     }
     size_t bytes = 0;
     void* workspace = nullptr;

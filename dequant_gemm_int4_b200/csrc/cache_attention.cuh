@@ -42,6 +42,7 @@
 // replayed with other lengths.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "cache.cuh"
@@ -1199,13 +1200,29 @@ __global__ void __launch_bounds__(256)
 
 // ---- Host side ------------------------------------------------------------
 
-// Query rows of a tile: the smallest of 8, 16 and 32 that holds the rows of an
-// average sequence (query tokens times ratio); 16 at most for 256 elements,
-// where the accumulators of 32 rows do not fit in registers.
+// Query rows of a tile, by the rows of an average sequence (query tokens times
+// ratio): 8 for up to 8; else 32 where an even number of tiles of 16 holds them
+// and 16 where an odd one does (32 sequences of 4096 tokens, 8 heads of 128:
+// 32 rows 94 us as one tile, 101 us as two; 48 rows 169 us as two tiles of 32,
+// 143 us as three of 16); 16 for 256 elements, where the accumulators of 32
+// rows do not fit in registers.
 inline int attention_row_tile(int head_dim, int64_t rows, int64_t batch, int ratio) {
   const int64_t r = (rows * ratio + batch - 1) / batch;
   if (r <= 8) return 8;
-  return r <= 16 || head_dim > 128 ? 16 : 32;
+  return head_dim > 128 || (r + 15) / 16 % 2 == 1 ? 16 : 32;
+}
+
+// Sets a kernel's dynamic shared memory once on each device.
+template <auto kKernel>
+cudaError_t allow_shared(int bytes) {
+  static std::atomic<bool> done[64];  // one array for each kernel
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 // The parts of a workspace.
@@ -1256,8 +1273,8 @@ int attention_blocks() {
 template <typename T, class C>
 cudaError_t launch_attention_cfg(const AttentionArgs& a, void* workspace, cudaStream_t stream) {
   const AttentionSpace ws = attention_space(workspace, a.batch, attention_blocks<C>(), C::RT, C::D);
-  auto kernel = attention_mma_kernel<T, C>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  constexpr auto kernel = attention_mma_kernel<T, C>;
+  cudaError_t e = allow_shared<kernel>(C::kSmem);
   if (e != cudaSuccess) return e;
   int shift = 0;
   while ((1 << shift) < a.cache.page_size) ++shift;

@@ -785,10 +785,10 @@ cudaError_t launch_typed(const AttentionArgs& a, void* workspace, cudaStream_t s
   uint32_t* status = status_word();
   if (status == nullptr) return cudaErrorInvalidSymbol;
   const AttentionSpace ws = attention_space(workspace, a.batch, num_sms(), kRows, D);
-  auto kernel = attention_prefill_kernel<T, D, ASYM>;
+  constexpr auto kernel = attention_prefill_kernel<T, D, ASYM>;
   constexpr int bytes = Smem<D>::kAlloc;
   static_assert(bytes <= 227 * 1024, "one block's shared memory");
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = allow_shared<kernel>(bytes);
   if (e != cudaSuccess) return e;
   int shift = 0;
   while ((1 << shift) < a.cache.page_size) ++shift;
