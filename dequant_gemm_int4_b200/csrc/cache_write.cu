@@ -9,8 +9,12 @@
 // with q = 0 (and z = 0) where s is 0 or infinite, and stored at the token's
 // slot.  Reading a slot gives q s or (q - z) s, rounded once.
 //
-// Both are bound by HBM for long runs of tokens and by launch latency for a
-// decoding step's few tokens.
+// A decoding step's few tokens cost a launch.  65536 tokens of 8 heads of 128 in
+// bf16 are read in 67 us, bound by HBM (5.0 TB/s of codes and values), and
+// written in 100 us, bound by instruction issue (325 for 16 elements of a warp's
+// 32 lanes: widening, extremes, correctly rounded quotients, packing).
+#include <type_traits>
+
 #include "cache.cuh"
 #include "internal.h"
 
@@ -28,6 +32,18 @@ __device__ __forceinline__ float quotient(float v, float s, float r) {
   return __fmaf_rn(__fmaf_rn(-q, s, v), r, q);
 }
 
+// fp32(v / N), correctly rounded, for finite v >= 0: one residual correction
+// with c = RN(1 / N) (Markstein, as above); where the residual could round (v
+// subnormal) the scale is 0 either way.  An infinite v stays infinite.
+template <int N>
+__device__ __forceinline__ float over(float v) {
+  constexpr float c = N == 7 ? 0.142857149f : 0.0666666701f;
+  static_assert(N == 7 || N == 15, "the schemes' divisors");
+  const float q = __fmul_rn(v, c);
+  const float r = __fmaf_rn(__fmaf_rn(-static_cast<float>(N), q, v), c, q);
+  return v < 0x1p127f ? r : __fdiv_rn(v, static_cast<float>(N));
+}
+
 // Scale and zero point of a group, and the codes of its elements.
 struct Coder {
   float s;         // the scale as stored
@@ -40,7 +56,7 @@ struct Coder {
   // lo, hi: the group's extremes (affine), or 0 and its absmax (symmetric).
   template <bool ASYM>
   __device__ __forceinline__ void set(float lo, float hi) {
-    const float d = ASYM ? __fdiv_rn(__fsub_rn(hi, lo), 15.0f) : __fdiv_rn(hi, 7.0f);
+    const float d = ASYM ? over<15>(__fsub_rn(hi, lo)) : over<7>(hi);
     bits = __half_as_ushort(__float2half_rn(d));
     s = f16_bits_to_float(bits);
     live = s > 0.0f && bits != 0x7C00u;
@@ -105,15 +121,19 @@ struct ReadArgs {
   int64_t tokens;
 };
 
-// A block of the fast kernels takes `per_block` whole tokens, whose 2 H rows
-// are cut into pieces of 16 elements, `per_row` = D / 16 of them: piece i of
-// the block belongs to row i / per_row, row r to token r / (2 H).  Divisions
-// by multiplication with m = ceil(2^32 / divisor), exact for the products
-// below 2^32 that occur (i < 2^16, divisors from 2 to 2^16).
+// A block of the fast kernels takes 2^tokens_log whole tokens, whose 2 H rows
+// are cut into pieces of 16 elements, `per_row` of them.  Piece i of the block
+// belongs to row r = i / per_row, the token r % 2^tokens_log and the key or value
+// head r >> tokens_log: neighbouring rows of a warp are neighbouring tokens of
+// one head, whose codes and scales are neighbours in the cache (with the heads
+// of one token side by side instead, reading 65536 tokens of 8 heads of 128 took
+// 78 us, not 67).  The division is a
+// multiplication with m = ceil(2^32 / per_row), exact for the products below
+// 2^32 that occur (i < 2^16, divisors from 2 to 2^16).
 struct Pieces {
   uint32_t per_row, per_row_m;
-  uint32_t rows, rows_m;  // 2 H
-  uint32_t per_block;     // tokens
+  uint32_t rows;  // 2 H
+  uint32_t tokens_log;
 };
 constexpr int kMaxBlockTokens = 64;
 
@@ -135,91 +155,113 @@ __device__ __forceinline__ void find_rows(const CacheView& c, const int64_t* slo
   __syncthreads();
 }
 
+// 16 elements as they are stored, and widened (exactly).
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Raw16 {
+  static constexpr int kVecs = sizeof(T) == 4 ? 4 : 2;
+  uint4 x[kVecs];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < kVecs; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
   }
-}
-template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = f16_bits_to_float(w[i] & 0xFFFFu);
-    v[2 * i + 1] = f16_bits_to_float(w[i] >> 16);
+    for (int i = 0; i < kVecs; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-}
+  __device__ __forceinline__ void widen(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (sizeof(T) == 4) {
+          v[4 * i + k] = __uint_as_float(w[k]);
+        } else if (std::is_same<T, __half>::value) {
+          v[8 * i + 2 * k] = f16_bits_to_float(w[k] & 0xFFFFu);
+          v[8 * i + 2 * k + 1] = f16_bits_to_float(w[k] >> 16);
+        } else {
+          v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+          v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
+      }
+    }
+  }
+};
 
-// D a multiple of 16, group = 16 LPG dividing D with LPG a power of two <= 32,
-// every source row 16-byte aligned, packed 8-byte aligned.  A thread codes 16
-// consecutive elements of one row (two 16-byte loads of 16-bit elements, one
-// 8-byte store); the LPG lanes of a group, neighbours in one warp since LPG
-// divides D / 16, find its extremes with shuffles.
+// group a multiple of 16 up to 512 that divides D, every source row 16-byte
+// aligned, packed 8-byte aligned.  A thread codes 16 consecutive elements of
+// one row (two 16-byte loads of 16-bit elements, one 8-byte store); a group has
+// `lpg` lanes, the next power of two from group / 16 on, which lie in one warp
+// and find its extremes with shuffles (the lanes past group / 16 only take
+// part in those).  The next piece is loaded while this one is coded.
 template <typename T, bool ASYM>
 __global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant__ WriteArgs a,
-                                                          const Pieces p, const int lpg) {
+                                                          const Pieces p, const int lpg_log) {
   const CacheView& c = a.cache;
   __shared__ int64_t s_rows[kMaxBlockTokens];
-  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * p.per_block;
-  find_rows(c, a.slots, token0, a.tokens, p.per_block, s_rows);
-  const uint32_t total = p.per_block * p.rows * p.per_row;
-  // Whole warps take part in every step, so that the shuffles are uniform.
-  for (uint32_t base = 0; base < total; base += blockDim.x) {
+  const int64_t token0 = static_cast<int64_t>(blockIdx.x) << p.tokens_log;
+  find_rows(c, a.slots, token0, a.tokens, 1 << p.tokens_log, s_rows);
+  const uint32_t total = (p.rows << p.tokens_log) * p.per_row;
+  const int lpg = 1 << lpg_log;
+  struct Piece {
+    Raw16<T> raw;
+    int64_t at;  // its row in the cache, -1: none
+    int group, d;
+  };
+  auto load = [&](uint32_t base, Piece& x) {
     const uint32_t i = base + threadIdx.x;
-    const uint32_t r = __umulhi(i, p.per_row_m), d = (i - r * p.per_row) * 16;
-    const uint32_t tok = __umulhi(r, p.rows_m), row = r - tok * p.rows;
-    const int64_t at0 = i < total ? s_rows[tok] : -1;
+    const uint32_t r = __umulhi(i, p.per_row_m), in_row = i - r * p.per_row;
+    const uint32_t row = r >> p.tokens_log, tok = r - (row << p.tokens_log);
+    x.group = in_row >> lpg_log;
+    const int in_group = (in_row & (lpg - 1)) * 16;
+    x.d = x.group * c.group + in_group;
+    x.at = i < total && in_group < c.group ? s_rows[tok] : -1;
+    x.raw.clear();
+    if (x.at < 0) return;
+    x.at += static_cast<int64_t>(row) * c.page_size;  // values follow the keys of all heads
     const int kv = row >= static_cast<uint32_t>(c.heads) ? 1 : 0;
-    const int h = row - kv * c.heads;
+    const T* src = static_cast<const T*>(kv ? a.src[1] : a.src[0]) +
+                   (token0 + tok) * (kv ? a.token_stride[1] : a.token_stride[0]) +
+                   static_cast<int>(row - kv * c.heads) * (kv ? a.head_stride[1] : a.head_stride[0]) + x.d;
+    x.raw.load(src);
+  };
+  // Whole warps take part in every step, so that the shuffles are uniform.
+  Piece x;
+  load(0, x);
+  for (uint32_t base = 0; base < total; base += blockDim.x) {
+    Piece next;
+    next.at = -1;
+    if (base + blockDim.x < total) load(base + blockDim.x, next);
     float v[16];
-    if (at0 >= 0) {
-      const T* src = static_cast<const T*>(kv ? a.src[1] : a.src[0]) +
-                     (token0 + tok) * (kv ? a.token_stride[1] : a.token_stride[0]) +
-                     h * (kv ? a.head_stride[1] : a.head_stride[0]) + d;
-      load8<T>(src, *reinterpret_cast<float(*)[8]>(v));
-      load8<T>(src + 8, *reinterpret_cast<float(*)[8]>(v + 8));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = 0.0f;
-    }
+    x.raw.widen(v);
     float lo = ASYM ? v[0] : 0.0f, hi = ASYM ? v[0] : fabsf(v[0]);
 #pragma unroll
     for (int k = 1; k < 16; ++k) {
       if (ASYM) lo = fminf(lo, v[k]);
       hi = fmaxf(hi, ASYM ? v[k] : fabsf(v[k]));
     }
+    if (ASYM && x.at < 0) {  // nothing of the group: neutral
+      lo = __int_as_float(0x7F800000);
+      hi = __int_as_float(0xFF800000);
+    }
     for (int off = 1; off < lpg; off <<= 1) {
       if (ASYM) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
     }
-    if (at0 < 0) continue;
-    Coder q;
-    q.set<ASYM>(lo, hi);
-    uint2 word = make_uint2(0u, 0u);
-    q.codes8<ASYM>(v, word.x);
-    q.codes8<ASYM>(v + 8, word.y);
-    const int64_t at = at0 + static_cast<int64_t>(row) * c.page_size;  // values follow the keys of all heads
-    *reinterpret_cast<uint2*>(c.packed + at * c.row_bytes + (d >> 1)) = word;
-    if ((threadIdx.x & (lpg - 1)) == 0) {
-      const int64_t g = at * c.groups + d / c.group;
-      c.scales[g] = q.bits;
-      if (ASYM) c.zeros[g] = static_cast<uint8_t>(q.z);
+    if (x.at >= 0) {
+      Coder q;
+      q.set<ASYM>(lo, hi);
+      uint2 word = make_uint2(0u, 0u);
+      q.codes8<ASYM>(v, word.x);
+      q.codes8<ASYM>(v + 8, word.y);
+      *reinterpret_cast<uint2*>(c.packed + x.at * c.row_bytes + (x.d >> 1)) = word;
+      if ((threadIdx.x & (lpg - 1)) == 0) {
+        const int64_t g = x.at * c.groups + x.group;
+        c.scales[g] = q.bits;
+        if (ASYM) c.zeros[g] = static_cast<uint8_t>(q.z);
+      }
     }
+    x = next;
   }
 }
 
@@ -293,7 +335,7 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const fl
     const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 template <>
 __device__ __forceinline__ void store8<__half>(__half* p, const float (&v)[8]) {
@@ -313,14 +355,14 @@ template <typename TO, bool ASYM>
 __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ ReadArgs a, const Pieces p) {
   const CacheView& c = a.cache;
   __shared__ int64_t s_rows[kMaxBlockTokens];
-  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * p.per_block;
-  find_rows(c, a.slots, token0, a.tokens, p.per_block, s_rows);
-  const int64_t here = a.tokens - token0;
-  const uint32_t total = (here < p.per_block ? static_cast<uint32_t>(here) : p.per_block) * p.rows * p.per_row;
+  const int64_t token0 = static_cast<int64_t>(blockIdx.x) << p.tokens_log;
+  find_rows(c, a.slots, token0, a.tokens, 1 << p.tokens_log, s_rows);
+  const uint32_t total = (p.rows << p.tokens_log) * p.per_row;
 #pragma unroll 4
   for (uint32_t i = threadIdx.x; i < total; i += blockDim.x) {
     const uint32_t r = __umulhi(i, p.per_row_m), d = (i - r * p.per_row) * 16;
-    const uint32_t tok = __umulhi(r, p.rows_m), row = r - tok * p.rows;
+    const uint32_t row = r >> p.tokens_log, tok = r - (row << p.tokens_log);
+    if (token0 + tok >= a.tokens) continue;
     const int64_t at0 = s_rows[tok];
     const int kv = row >= static_cast<uint32_t>(c.heads) ? 1 : 0;
     const int h = row - kv * c.heads;
@@ -387,32 +429,32 @@ bool multiple_of(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t
 
 // The blocks of a fast kernel: about four pieces a thread, fewer where that
 // would leave SMs without a block.  False where the sizes are out of its range.
-bool cut(const CacheView& c, int64_t tokens, Pieces* p, int64_t* grid) {
-  const int64_t per_row = c.head_dim / 16, rows = 2LL * c.heads;
+bool cut(const CacheView& c, int64_t tokens, int64_t per_row, Pieces* p, int64_t* grid) {
+  const int64_t rows = 2LL * c.heads;
   if (c.head_dim % 16 != 0 || c.group % 16 != 0 || per_row < 2 || rows * per_row > 8192) return false;
-  int64_t n = 1024 / (rows * per_row);
   const int64_t spread = (tokens + 4 * num_sms() - 1) / (4 * num_sms());
-  n = n < spread ? n : spread;
-  n = n < 1 ? 1 : (n < kMaxBlockTokens ? n : kMaxBlockTokens);
+  uint32_t log = 0;
+  while ((2 << log) <= kMaxBlockTokens && (2 << log) * rows * per_row <= 1024 && (2 << log) <= spread) ++log;
   *p = {static_cast<uint32_t>(per_row), static_cast<uint32_t>(((1LL << 32) + per_row - 1) / per_row),
-        static_cast<uint32_t>(rows), static_cast<uint32_t>(((1LL << 32) + rows - 1) / rows), static_cast<uint32_t>(n)};
-  *grid = (tokens + n - 1) / n;
+        static_cast<uint32_t>(rows), log};
+  *grid = (tokens + (1LL << log) - 1) >> log;
   return *grid <= 0x7FFFFFFF;
 }
 
 template <typename T, bool ASYM>
 cudaError_t write_typed(const WriteArgs& a, cudaStream_t stream) {
   const CacheView& c = a.cache;
-  const int lpg = c.group / 16;
+  int lpg_log = 0;
+  while ((16 << lpg_log) < c.group) ++lpg_log;
   Pieces p;
   int64_t grid;
-  bool fast = cut(c, a.tokens, &p, &grid) && lpg <= 32 && (lpg & (lpg - 1)) == 0 && c.head_dim % c.group == 0 &&
-              multiple_of(c.packed, 8);
+  bool fast = c.head_dim % c.group == 0 && lpg_log <= 5 && multiple_of(c.packed, 8) &&
+              cut(c, a.tokens, static_cast<int64_t>(c.groups) << lpg_log, &p, &grid);
   for (int kv = 0; kv < 2; ++kv)
     fast = fast && multiple_of(a.src[kv], 16) && (a.token_stride[kv] * sizeof(T)) % 16 == 0 &&
            (a.head_stride[kv] * sizeof(T)) % 16 == 0;
   if (fast) {
-    cache_write_kernel<T, ASYM><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a, p, lpg);
+    cache_write_kernel<T, ASYM><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a, p, lpg_log);
     return cudaGetLastError();
   }
   const int64_t warps = a.tokens * 2 * c.heads;
@@ -425,7 +467,7 @@ cudaError_t read_typed(const ReadArgs& a, cudaStream_t stream) {
   const CacheView& c = a.cache;
   Pieces p;
   int64_t grid;
-  if (cut(c, a.tokens, &p, &grid) && multiple_of(c.packed, 8) && multiple_of(a.dst[0], 16) && multiple_of(a.dst[1], 16)) {
+  if (cut(c, a.tokens, c.head_dim / 16, &p, &grid) && multiple_of(c.packed, 8) && multiple_of(a.dst[0], 16) && multiple_of(a.dst[1], 16)) {
     cache_read_kernel<TO, ASYM><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a, p);
     return cudaGetLastError();
   }
