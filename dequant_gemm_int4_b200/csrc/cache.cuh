@@ -94,7 +94,7 @@ struct AttentionArgs {
   // tokens sees (none where hi <= lo).
   __device__ __forceinline__ void visible(int pos, int len, int& lo, int& hi) const {
     hi = causal != 0 ? max(min(pos + 1, len), 0) : len;
-    lo = window > 0 ? max(pos - window + 1, 0) : 0;
+    lo = window > 0 && pos >= window ? pos - window + 1 : 0;
   }
   // The sequence that holds query row t, or -1.
   __device__ __forceinline__ int sequence_of(int t) const {

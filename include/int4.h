@@ -448,7 +448,9 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * workspace_bytes == 0 where that size is 0.  Calls that may overlap in time
  * need different workspaces, graphs that may be replayed at the same time too.
  * Nothing else is kept between calls; the lengths, the table and the slots are
- * read on the device, so a captured call can be replayed with others.
+ * read on the device, so a captured call can be replayed with others.  The
+ * outputs are undefined after int4_device_status has reported
+ * INT4_ERR_TIMEOUT for the call.
  */
 int int4_cache_attention(const int4_cache* cache, const void* q, int64_t q_token_stride,
                          int64_t q_head_stride, int32_t dtype, int64_t rows, int32_t q_heads,

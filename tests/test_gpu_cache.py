@@ -363,6 +363,56 @@ def test_attention_nan_in_a_query_stays_in_its_rows(path, bad):
     assert torch.equal(got[0][keep], clean[0][keep]) and torch.equal(got[1][keep], clean[1][keep])
 
 
+def test_attention_many_rows_strided_and_unaligned():
+    """The kernel for many rows on queries inside wider rows, aligned and not."""
+    q, packed, scales, zeros, table, lens, group = attention_setup(lens=(300, 200))
+    q = torch.randn((150, 8, 128), generator=torch.Generator().manual_seed(1)).cuda().bfloat16()
+    starts = torch.tensor([0, 100, 150], dtype=torch.int32, device="cuda")
+    call = lambda x: q4.int4_cache_attention(x, packed, scales, table, lens, group, zeros=zeros, q_starts=starts,  # noqa: E731
+                                             return_lse=True, path=q4.PATH_PREFILL)
+    want = call(q)
+    assert_attention_close(want, attention_ref(q, packed, scales, zeros, table, [300, 200], [100, 50], group))
+    fused = torch.zeros(150, 20, 128, dtype=torch.bfloat16, device="cuda")
+    fused[:, 5:13] = q
+    wide = torch.zeros(150, 8, 131, dtype=torch.bfloat16, device="cuda")
+    wide[:, :, 3:] = q
+    for x in (fused[:, 5:13], wide[:, :, 3:]):
+        assert all(torch.equal(a, b) for a, b in zip(call(x), want))
+    # An output that is not 16-byte aligned: refused when forced, else another kernel's.
+    odd = torch.empty(150 * 8 * 128 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(150, 8, 128)
+    with pytest.raises(q4.Int4Error, match="cannot run"):
+        q4.int4_cache_attention(q, packed, scales, table, lens, group, zeros=zeros, q_starts=starts, out=odd,
+                                path=q4.PATH_PREFILL)
+    q4.int4_cache_attention(q, packed, scales, table, lens, group, zeros=zeros, q_starts=starts, out=odd)
+    assert_attention_close((odd, want[1]), attention_ref(q, packed, scales, zeros, table, [300, 200], [100, 50], group))
+
+
+@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE, q4.PATH_PREFILL])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_largest_window(path, causal):
+    """A window past every token, with queries before the first one."""
+    run_attention(1, 2, 64, 64, 16, [40, 3], [60, 9], torch.bfloat16, causal=causal, window=2 ** 31 + 5, path=path)
+
+
+@pytest.mark.parametrize("pages", [1, 2, 4, 8, 16, 33, 64])
+@pytest.mark.parametrize("batch, H", [(1, 1), (3, 8), (80, 8)])
+def test_attention_table_sizes(pages, batch, H):
+    """Tables with room for one step to many: joined in clusters of 1 to 8 blocks, or in shares; lengths from 0 to all of it."""
+    D, S = 64, 128
+    P = 40
+    packed, scales, zeros = random_cache(P, S, H, D, 64, False, seed=pages)
+    rng = np.random.default_rng(pages + batch)
+    table = torch.from_numpy(rng.integers(0, P, (batch, pages)).astype(np.int32)).cuda()  # pages may be shared
+    lens = [int(n) for n in rng.integers(0, pages * S + 1, batch)]
+    lens[0] = pages * S
+    if batch > 1:
+        lens[1] = 0
+    q = torch.from_numpy(rng.normal(size=(2 * batch, 3 * H, D)).astype(np.float32)).cuda().bfloat16()
+    got = q4.int4_cache_attention(q, packed, scales, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), 64,
+                                  zeros=zeros, return_lse=True, path=q4.PATH_DECODE)
+    assert_attention_close(got, attention_ref(q, packed, scales, zeros, table, lens, [2] * batch, 64))
+
+
 def test_attention_value_scales_of_all_sizes():
     """Value scales from fp16 subnormals to its largest, growing and shrinking along the sequence."""
     for affine in (False, True):
