@@ -173,16 +173,16 @@ bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out,
          multiple_of(c.zeros, 16) && multiple_of(out, 8);
 }
 
-// The tcgen05 kernel takes heads of 64 or 128 elements in one group, and
-// outputs aligned to 16 bytes.
+// The tcgen05 kernel takes heads of 64, 96 or 128 elements in one group or in
+// groups of 32 or 64, and outputs aligned to 16 bytes.
 bool cache_prefill_supported(const CacheView& c, DType t, const void* out, int64_t rows, int64_t batch, int ratio,
                              int64_t max_pages) {
-  return (c.head_dim == 64 || c.head_dim == 128) && c.group == c.head_dim && multiple_of(out, 16) &&
+  return (c.head_dim == 64 || c.head_dim == 96 || c.head_dim == 128) && multiple_of(out, 16) &&
          cache_attention_mma_supported(c, t, out, rows, batch, ratio, max_pages);
 }
 
 size_t cache_prefill_workspace(const CacheView& c, int64_t batch) {
-  return attention_space_bytes(batch, num_sms(), cache_prefill_row_tile(), c.head_dim);
+  return attention_space_bytes(batch, num_sms(), kPrefillRowTile, c.head_dim);
 }
 
 size_t cache_attention_mma_workspace(const CacheView& c, int64_t rows, int64_t batch, int ratio) {
@@ -196,6 +196,14 @@ size_t cache_attention_mma_workspace(const CacheView& c, int64_t rows, int64_t b
     default: blocks = cache_attention_blocks_256(c.group, asym, rt); break;
   }
   return attention_space_bytes(batch, blocks, rt, c.head_dim);
+}
+
+cudaError_t launch_cache_prefill(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream) {
+  switch (a.cache.head_dim) {
+    case 64: return launch_cache_prefill_64(a, t, workspace, stream);
+    case 96: return launch_cache_prefill_96(a, t, workspace, stream);
+    default: return launch_cache_prefill_128(a, t, workspace, stream);
+  }
 }
 
 cudaError_t launch_cache_attention_mma(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream) {

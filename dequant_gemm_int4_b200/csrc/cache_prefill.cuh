@@ -19,20 +19,35 @@
 //                and its value row
 //   warps 8-15   softmax: thread r of group m owns query row r of tile m
 //
-// Operands are exact: q in fp16 after a power-of-two scaling of its row (see
-// cache_attention.cuh), keys and values as the integers n - z.  The token's
-// key scale multiplies its column of S in fp32, its value scale the weight,
-// W = 2^x P s rounded to fp16 once (x: a power of two that keeps it in range).
-// So one group a head is required here (group = head_dim).  S, the maximum and
+// q enters in fp16 after a power-of-two scaling of its row (see
+// cache_attention.cuh).  With one group a head, keys and values are the integers
+// n - z, exactly: the token's key scale multiplies its column of S in fp32, its
+// value scale the weight, W = 2^x P s rounded to fp16 once (x: a power of two
+// that keeps it in range).  With several groups, the power of two u of the
+// token's largest scale takes the scale's place there, and the elements are
+// (n - z) s / u: values rounded to fp16, keys as the sum of two fp16 numbers, a
+// product each, which hold all of their at most 16 bits (to 2^-20 u, where the
+// scales of a token's groups differ by more than 2^9); the second takes the
+// place of the keys' second stage in shared memory.  S, the maximum and
 // the sum are fp32; O is fp32 in tensor memory.  Weights are taken relative to a
 // reference that follows the row's maximum only when that has passed it by
 // more than a factor 2^8: a half tile's weights are computed at once under the
 // old reference, and only where that turns out too far behind, or some row
 // does not see all tokens, with the maximum first.
 //
+// What bounds it.  1789 queries of two prompts on 8192 and 6757 tokens, 64 heads
+// of 128 on 8: 577 us, of 256 us at the tensor pipe's measured rate.  The MMAs
+// alone take 250 us, with the hand-overs between S, softmax and W V and a
+// trivial softmax 440 us: each change between the two products drains the pipe
+// for about 300 cycles, and tensor memory has no room for longer products.
+// With groups the expansion bounds it: 8 heads of 128, 2048 rows of one sequence
+// of 16384 tokens take 206 us in one group and 322 us in groups of 32.
+//
 // Inside blocks of 8 elements, keys and queries are stored in the order 0, 4,
 // 1, 5, 2, 6, 3, 7 in which a code word expands pair by pair; O's columns come
 // out in that order and are put right when they are stored.
+#pragma once
+
 #include <type_traits>
 
 #include "cache.cuh"
@@ -44,7 +59,7 @@ namespace int4lib {
 
 namespace {
 
-constexpr int kRows = 256;     // query rows of an item
+constexpr int kRows = kPrefillRowTile;  // query rows of an item
 constexpr int kTok = 128;      // tokens of a tile
 constexpr int kThreadsP = 512;
 constexpr int kScaleRing = 4;  // tiles of column scales held
@@ -63,7 +78,7 @@ struct Bars {
 template <int D>
 struct Smem {
   static constexpr int kSub = 128 * 128;         // 128 rows of 128 bytes: 64 elements, 128-byte swizzle
-  static constexpr int kTile = D / 64 * kSub;    // 128 rows of D elements
+  static constexpr int kTile = (D + 63) / 64 * kSub;  // 128 rows of D elements
   static constexpr int offQ = 0;                 // two row tiles
   static constexpr int offK = offQ + 2 * kTile;  // two stages
   static constexpr int offV = offK + 2 * kTile;  // two stages
@@ -188,11 +203,12 @@ __device__ __forceinline__ uint4 expand(uint32_t w, uint32_t b1, uint32_t b16) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <typename T, int D, bool ASYM>
+template <typename T, int D, bool ASYM, bool GROUPED>
 __global__ void __launch_bounds__(kThreadsP, 1)
     attention_prefill_kernel(const __grid_constant__ AttentionArgs a, const AttentionSpace ws, const int page_shift,
                              uint32_t* status) {
   using L = Smem<D>;
+  constexpr int kStagesK = GROUPED ? 1 : 2;
   constexpr float kNegInf = -__builtin_huge_valf();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -323,10 +339,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       auto s_mma = [&](int m, int stage, int h) {
         const uint32_t k_lo = k_lo0 + stage * (L::kTile >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * L::kSub + (k % 4) * 32;
-          mma_ss(lead, tmem + m * kTok + h * 64, desc_at(q_lo, m * L::kTile + off), desc_at(k_lo, h * 8192 + off), id_s,
-                 k == 0 ? 0u : 1u);
+        for (int part = 0; part < (GROUPED ? 2 : 1); ++part) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * L::kSub + (k % 4) * 32;
+            mma_ss(lead, tmem + m * kTok + h * 64, desc_at(q_lo, m * L::kTile + off),
+                   desc_at(k_lo, part * L::kTile + h * 8192 + off), id_s, part == 0 && k == 0 ? 0u : 1u);
+          }
         }
         commit(lead, bar(bars->s_full[m][h]));
       };
@@ -345,11 +364,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (!(ok = wait_all(bar(bars->q_full), item & 1u, wc))) break;
         const int n = s_steps[item & 1u];
         if (n == 0) break;
-        if (!(ok = wait_all(bar(bars->k_full[t & 1]), (t >> 1) & 1u, wc))) break;
+        if (!(ok = wait_all(bar(bars->k_full[t % kStagesK]), (t / kStagesK) & 1u, wc))) break;
         ptx::tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s_mma(i & 1, t & 1, i >> 1);
-        commit(lead, bar(bars->k_empty[t & 1]));
+        for (int i = 0; i < 4; ++i) s_mma(i & 1, t % kStagesK, i >> 1);
+        commit(lead, bar(bars->k_empty[t % kStagesK]));
         for (int j = 0; ok && j < n; ++j, ++t) {
           ok = wait_all(bar(bars->v_full[t & 1]), (t >> 1) & 1u, wc);
 #pragma unroll
@@ -363,16 +382,16 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             // step behind, so that it does not wait for it.
             if (i == 0) {
               if (j > 0) {
-                s_mma(1, t & 1, 1);
-                commit(lead, bar(bars->k_empty[t & 1]));
+                s_mma(1, t % kStagesK, 1);
+                commit(lead, bar(bars->k_empty[t % kStagesK]));
               }
             } else if (j + 1 < n) {
               if (i == 1) {
-                ok = wait_all(bar(bars->k_full[(t + 1) & 1]), ((t + 1) >> 1) & 1u, wc);
+                ok = wait_all(bar(bars->k_full[(t + 1) % kStagesK]), ((t + 1) / kStagesK) & 1u, wc);
                 if (!ok) break;
                 ptx::tc_fence_after();
               }
-              s_mma((i - 1) & 1, (t + 1) & 1, (i - 1) >> 1);
+              s_mma((i - 1) & 1, (t + 1) % kStagesK, (i - 1) >> 1);
             }
           }
           if (!ok) break;
@@ -407,30 +426,77 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       if (id < 0 || id >= cache.pages) return -1;
       return id * page_rows + (static_cast<int64_t>(w.h) << page_shift) + (tok & (cache.page_size - 1));
     };
+    // Scales (and zero points) of a row: one, or one for each 32 elements.
+    constexpr int kScales = GROUPED ? kVec : 1;
+    const int per_scale = cache.group >> 6;  // 0 or 1: log2 of the 32-element blocks of a group
     struct Row {
       uint4 v[kVec];
-      uint32_t s, z;
+      uint32_t s[kScales], z[kScales];
+      // Bits of the largest finite scale, and whether all are finite.
+      __device__ __forceinline__ uint32_t top(bool& finite) const {
+        uint32_t m = 0u;
+        finite = true;
+#pragma unroll
+        for (int i = 0; i < kScales; ++i) {
+          if ((s[i] & 0x7C00u) == 0x7C00u)
+            finite = false;
+          else
+            m = max(m, s[i] & 0x7FFFu);
+        }
+        return m;
+      }
     };
     auto load = [&](int64_t row, Row& x) {
 #pragma unroll
       for (int i = 0; i < kVec; ++i)
         x.v[i] = row < 0 ? make_uint4(0u, 0u, 0u, 0u)
                          : __ldg(reinterpret_cast<const uint4*>(cache.packed + row * (D / 2)) + i);
-      x.s = row < 0 ? 0u : __ldg(cache.scales + row);
-      x.z = ASYM && row >= 0 ? __ldg(cache.zeros + row) : 0u;
+#pragma unroll
+      for (int i = 0; i < kScales; ++i) {
+        const int64_t at = GROUPED ? row * cache.groups + (i >> per_scale) : row;
+        x.s[i] = row < 0 ? 0u : __ldg(cache.scales + at);
+        x.z[i] = ASYM && row >= 0 ? __ldg(cache.zeros + at) : 0u;
+      }
     };
-    auto store = [&](const Row& x, uint32_t at) {
-      const uint32_t z = ASYM ? x.z : 8u;
-      // -(1024 + z) and -(64 + z), exact.
-      const uint32_t b1 = (0xE400u + z) * 0x00010001u;
-      const uint32_t b16 = __half_as_ushort(__int2half_rn(-64 - static_cast<int>(z))) * 0x00010001u;
+    // What multiplies the token's column in fp32: its scale, or the power of two
+    // of its largest one.
+    auto column = [&](const Row& x, uint32_t top) {
+      return GROUPED ? __uint_as_float((127u - 15u + max(top >> 10, 1u)) << 23) : f16_bits_to_float(x.s[0]);
+    };
+    auto store = [&](const Row& x, uint32_t at, uint32_t top, bool two_parts) {
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
+        const uint32_t z = ASYM ? x.z[GROUPED ? i : 0] : 8u;
+        // -(1024 + z) and -(64 + z), exact.
+        const uint32_t b1 = (0xE400u + z) * 0x00010001u;
+        const uint32_t b16 = __half_as_ushort(__int2half_rn(-64 - static_cast<int>(z))) * 0x00010001u;
+        // The scale over u, in [0, 2); 0 for one that is not finite.
+        uint32_t ratio = 0u;
+        if (GROUPED && (x.s[GROUPED ? i : 0] & 0x7C00u) != 0x7C00u) {
+          const float u_inv = __uint_as_float((127u + 15u - max(top >> 10, 1u)) << 23);
+          ratio = __half_as_ushort(__float2half_rn(f16_bits_to_float(x.s[GROUPED ? i : 0]) * u_inv)) * 0x00010001u;
+        }
         const uint32_t words[4] = {x.v[i].x, x.v[i].y, x.v[i].z, x.v[i].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int c = 4 * i + k;
-          ptx::sts128(at + (c >> 3) * L::kSub + r * 128 + (((c & 7) ^ sw) << 4), expand<ASYM>(words[k], b1, b16));
+          const uint32_t to = at + (c >> 3) * L::kSub + r * 128 + (((c & 7) ^ sw) << 4);
+          const uint4 q = expand<ASYM>(words[k], b1, b16);
+          if (!GROUPED) {
+            ptx::sts128(to, q);
+            continue;
+          }
+          const uint32_t n[4] = {q.x, q.y, q.z, q.w};
+          uint32_t y[4], rest[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] = attn::mul_half2(n[e], ratio);
+            // (n - z) s / u less what was kept of it: exact.
+            if (two_parts)
+              asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(rest[e]) : "r"(n[e]), "r"(ratio), "r"(y[e] ^ 0x80008000u));
+          }
+          ptx::sts128(to, make_uint4(y[0], y[1], y[2], y[3]));
+          if (two_parts) ptx::sts128(to + L::kTile, make_uint4(rest[0], rest[1], rest[2], rest[3]));
         }
       }
     };
@@ -446,33 +512,36 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       load(row < 0 ? row : row + to_values, vx);
       for (int j = 0; j < n; ++j, ++t) {
         const int64_t row_after = j + 2 < n ? find(base + (j + 2) * kTok) : -1;
-        const bool finite = (vx.s & 0x7C00u) != 0x7C00u;
+        bool k_finite, v_finite;
+        const uint32_t k_top = kx.top(k_finite), v_top = vx.top(v_finite);
         const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
-        const uint32_t bad = __ballot_sync(0xffffffffu, !finite);
-        const uint32_t top = __reduce_max_sync(0xffffffffu, finite ? vx.s & 0x7FFFu : 0u);  // orders as the scales do
-        const float ks = f16_bits_to_float(kx.s), vs = finite ? f16_bits_to_float(vx.s) : 0.0f;
+        const uint32_t bad = __ballot_sync(0xffffffffu, !v_finite);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, v_top);  // orders as the scales do
+        // A key scale that is not finite gives NaN, as its values do.
+        const float ks = k_finite ? column(kx, k_top) : __int_as_float(0x7FC00000);
+        const float vs = v_finite ? column(vx, v_top) : 0.0f;
         // Keys.  The stage's last reader finished (first use: at once); the
         // scales' entry was last used four tiles ago, by a softmax that has
         // since handed on a later tile.
-        if (!(ok = wait_all(bar(bars->k_empty[t & 1]), ((t >> 1) & 1u) ^ 1u, wc))) break;
+        if (!(ok = wait_all(bar(bars->k_empty[t % kStagesK]), ((t / kStagesK) & 1u) ^ 1u, wc))) break;
         const int ring = t & (kScaleRing - 1);
-        s_scale[(ring * 2) * kTok + r] = ks + ks * 0.0f;  // an infinite scale gives NaN, as its values do
+        s_scale[(ring * 2) * kTok + r] = ks;
         s_scale[(ring * 2 + 1) * kTok + r] = vs;
         if (lane == 0) {
           s_bits[ring].live[warp - 4] = live;
           s_bits[ring].bad[warp - 4] = bad;
           s_bits[ring].top[warp - 4] = top;
         }
-        store(kx, ptx::smem_u32(smem + L::offK + (t & 1) * L::kTile));
+        store(kx, ptx::smem_u32(smem + L::offK + (t % kStagesK) * L::kTile), k_top, GROUPED);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive(bar(bars->sc_full[ring]));
-          ptx::mbar_arrive(bar(bars->k_full[t & 1]));
+          ptx::mbar_arrive(bar(bars->k_full[t % kStagesK]));
         }
         if (j + 1 < n) load(row_next, kx);
         if (!(ok = wait_all(bar(bars->v_empty[t & 1]), ((t >> 1) & 1u) ^ 1u, wc))) break;
-        store(vx, ptx::smem_u32(smem + L::offV + (t & 1) * L::kTile));
+        store(vx, ptx::smem_u32(smem + L::offV + (t & 1) * L::kTile), v_top, false);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(bars->v_full[t & 1]));
@@ -780,12 +849,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   }
 }
 
-template <typename T, int D, bool ASYM>
-cudaError_t launch_typed(const AttentionArgs& a, void* workspace, cudaStream_t stream) {
+template <typename T, int D, bool ASYM, bool GROUPED>
+cudaError_t launch_prefill_typed(const AttentionArgs& a, void* workspace, cudaStream_t stream) {
   uint32_t* status = status_word();
   if (status == nullptr) return cudaErrorInvalidSymbol;
   const AttentionSpace ws = attention_space(workspace, a.batch, num_sms(), kRows, D);
-  constexpr auto kernel = attention_prefill_kernel<T, D, ASYM>;
+  constexpr auto kernel = attention_prefill_kernel<T, D, ASYM, GROUPED>;
   constexpr int bytes = Smem<D>::kAlloc;
   static_assert(bytes <= 227 * 1024, "one block's shared memory");
   cudaError_t e = allow_shared<kernel>(bytes);
@@ -798,20 +867,22 @@ cudaError_t launch_typed(const AttentionArgs& a, void* workspace, cudaStream_t s
   return launch_attention_join_items<T>(a, ws, kRows, stream);
 }
 
-template <typename T>
-cudaError_t launch_any(const AttentionArgs& a, void* workspace, cudaStream_t stream) {
+template <typename T, int D>
+cudaError_t launch_prefill_scheme(const AttentionArgs& a, void* workspace, cudaStream_t stream) {
   const bool asym = a.cache.zeros != nullptr;
-  if (a.cache.head_dim == 64)
-    return asym ? launch_typed<T, 64, true>(a, workspace, stream) : launch_typed<T, 64, false>(a, workspace, stream);
-  return asym ? launch_typed<T, 128, true>(a, workspace, stream) : launch_typed<T, 128, false>(a, workspace, stream);
+  if (a.cache.group == D)
+    return asym ? launch_prefill_typed<T, D, true, false>(a, workspace, stream)
+                : launch_prefill_typed<T, D, false, false>(a, workspace, stream);
+  return asym ? launch_prefill_typed<T, D, true, true>(a, workspace, stream)
+              : launch_prefill_typed<T, D, false, true>(a, workspace, stream);
+}
+
+template <int D>
+cudaError_t launch_prefill(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream) {
+  return t == DType::BF16 ? launch_prefill_scheme<__nv_bfloat16, D>(a, workspace, stream)
+                          : launch_prefill_scheme<__half, D>(a, workspace, stream);
 }
 
 }  // namespace
-
-int cache_prefill_row_tile() { return kRows; }
-
-cudaError_t launch_cache_prefill(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream) {
-  return t == DType::BF16 ? launch_any<__nv_bfloat16>(a, workspace, stream) : launch_any<__half>(a, workspace, stream);
-}
 
 }  // namespace int4lib

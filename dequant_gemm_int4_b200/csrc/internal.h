@@ -100,18 +100,26 @@ bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out,
                                    int ratio, int64_t max_pages);
 size_t cache_attention_mma_workspace(const CacheView& c, int64_t rows, int64_t batch, int ratio);
 cudaError_t launch_cache_attention_mma(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
-// cache_prefill.cu: the tcgen05 kernel for many query rows, its workspace
+// cache_prefill_<D>.cu: the tcgen05 kernel for many query rows, its workspace
 // likewise.
-int cache_prefill_row_tile();
-// Query rows of one head (tokens times ratio) of an average sequence from which
-// it is taken: 32 sequences of 4096 tokens, 8 heads of 128, take 175 us for 64
-// rows with the kernels for few rows and 210 us with this one, for 128 rows
-// 334 us and 219 us.
-constexpr int kPrefillRows = 80;
+constexpr int kPrefillRowTile = 256;
 bool cache_prefill_supported(const CacheView& c, DType t, const void* out, int64_t rows, int64_t batch, int ratio,
                              int64_t max_pages);
 size_t cache_prefill_workspace(const CacheView& c, int64_t batch);
 cudaError_t launch_cache_prefill(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
+cudaError_t launch_cache_prefill_64(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
+cudaError_t launch_cache_prefill_96(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
+cudaError_t launch_cache_prefill_128(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
+// Query rows of one head (tokens times ratio) of an average sequence from which
+// it is taken.  32 sequences of 4096 tokens, 8 heads, us with the kernels for
+// few rows and with this one:
+//   rows                 64          96         128         256
+//   128, one group    175 / 209   256 / 213   338 / 218   670 / 235
+//   128, groups of 64 201 / 342   295 / 346   388 / 349   768 / 366
+//   128, groups of 32 352 / 346   517 / 349   677 / 352  1345 / 369
+//   64, one group     132 / 185   187 / 186   246 / 189   489 / 200
+// For a single sequence of 16384 tokens the two meet near 128 rows (60 / 59 us).
+constexpr int kPrefillRows = 96;
 // cache_attention_<D>.cu: the kernels for heads of D elements; rt: query rows
 // of a tile.
 cudaError_t launch_cache_attention_64(const AttentionArgs& a, DType t, int rt, void* workspace, cudaStream_t stream);

@@ -428,9 +428,13 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * fp32 q so are the products.  For bf16 and fp16 q the products run on tensor
  * cores: q and the codes exactly (elements of q below 2^-24 of the row's
  * largest to 2^-38 of it), the weights exp(S_j - max) s_j, s_j the value
- * scales, in fp16: off by at most 2^-11 of themselves, or, where they are more
- * than 2^20 below the largest, 2^-32 of that.  Deterministic for given sizes,
- * lengths and device.
+ * scales, in fp16 after two roundings, each off by at most 2^-11 of the value,
+ * or, below 2^-20 s, by 2^-32 s, where s is the largest value scale and lies
+ * between 2^-8 and 2^8 (2^-24 s for larger, 2^-40 for smaller ones).
+ * INT4_PATH_PREFILL rounds the weight once; with several groups a head it rounds
+ * the values too, by 2^-11 of themselves, or 2^-20 of the token's largest scale
+ * where that is more, and the keys by at most the latter.  Deterministic for given
+ * sizes, lengths and device.
  * NaN or infinity in a query makes its own rows NaN, a value scale that is not
  * finite the outputs (not the lse) of the rows that see its token.
  *
@@ -440,7 +444,7 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * 32 or 96), page_size a power of two from 16 on, max_pages * page_size <= 2^30
  * (and steps of 128 tokens over all heads below 2^30), packed, scales and zeros
  * 16-byte and out 8-byte aligned.  INT4_PATH_PREFILL, for many: of those,
- * head_dim 64 or 128 in one group, out 16-byte aligned.  A forced path that
+ * head_dim 64, 96 or 128, out 16-byte aligned.  A forced path that
  * cannot run the call returns INT4_ERR_UNSUPPORTED.
  *
  * workspace: at least int4_cache_attention_workspace_size bytes (else

@@ -66,9 +66,11 @@ def attention_ref(q, packed, scales, zeros, table, lens, counts, group, *, causa
     * S_j: at most D + 64 fp32 operations on terms that sum to at most
       A_j = |sm_scale| s_j sum_d |q_d| (|n_d| + |z|) <= 30 |sm_scale| max(s_j) sum |q_d|, each off
       by at most 2^-23 (the tensor core may truncate) of that: e = (D + 64) 2^-23 max A_j.
-    * p_j: 2 e (numerator and denominator), 2^-20 for the exponentials, and
-      2^-11 + 2^-11 / 2 for the fp16 rounding of the weight (half a unit is
-      2^-12; the scale by the largest keeps it normal down to 2^-29).
+    * p_j: 2 e (numerator and denominator), 2^-20 for the exponentials.
+    * p_j V_j: two roundings to fp16, of the weight and of its product with the
+      scale, or of the weight and of the value: 2^-11 each at worst.  They are
+      independent from token to token, and three quarters of their sum,
+      2^-11 * 1.5, is asked for.
     * the sums over j: at most len + 256 fp32 operations on terms that sum to
       at most sum_j p_j s_j 30.
     * out: half a unit of its type."""

@@ -181,7 +181,8 @@ def test_attention(D, group, dtype, path, affine, ratio, counts):
 
 
 @pytest.mark.parametrize("affine", [False, True])
-@pytest.mark.parametrize("D, dtype", [(64, "bf16"), (64, "f16"), (128, "bf16"), (128, "f16")])
+@pytest.mark.parametrize("D, group, dtype", [(64, 64, "bf16"), (64, 32, "f16"), (96, 96, "f16"), (96, 32, "bf16"),
+                                             (128, 128, "bf16"), (128, 128, "f16"), (128, 64, "f16"), (128, 32, "bf16")])
 @pytest.mark.parametrize("H, ratio, lens, counts", [
     (1, 1, [128], [128]),                       # one tile of keys, one of rows
     (1, 1, [1], [1]),
@@ -190,8 +191,8 @@ def test_attention(D, group, dtype, path, affine, ratio, counts):
     (3, 3, [1000], [333]),                      # a ratio that does not divide the tile
     (2, 1, [3000, 5], [600, 9]),                # a sequence of fewer tokens than queries
 ])
-def test_attention_many_rows(D, dtype, affine, H, ratio, lens, counts):
-    run_attention(H, ratio, D, D, 32, lens, counts, DTYPES[dtype], affine=affine, path=q4.PATH_PREFILL)
+def test_attention_many_rows(D, group, dtype, affine, H, ratio, lens, counts):
+    run_attention(H, ratio, D, group, 32, lens, counts, DTYPES[dtype], affine=affine, path=q4.PATH_PREFILL)
 
 
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 63, 65, 127, 128, 129, 255, 257, 1000, 4097])
@@ -415,15 +416,16 @@ def test_attention_table_sizes(pages, batch, H):
 
 def test_attention_value_scales_of_all_sizes():
     """Value scales from fp16 subnormals to its largest, growing and shrinking along the sequence."""
-    for affine in (False, True):
-        q, packed, scales, zeros, table, lens, group = attention_setup(H=1, ratio=8, lens=(600, 300), affine=affine)
+    for affine, group in ((False, 128), (True, 128), (False, 32), (True, 64)):
+        q, packed, scales, zeros, table, lens, group = attention_setup(H=1, ratio=8, lens=(600, 300), affine=affine, group=group)
         factor = torch.from_numpy(np.exp2(np.random.default_rng(2).integers(-13, 14, scales[:, 1].shape)).astype(np.float32)).cuda()
         scales[:, 1] = (scales[:, 1].float() * factor).half()
         for sm_scale in (0.02, 0.3):
-            got = q4.int4_cache_attention(q, packed, scales, table, lens, group, zeros=zeros, return_lse=True,
-                                          sm_scale=sm_scale, path=q4.PATH_DECODE)
             want = attention_ref(q, packed, scales, zeros, table, [600, 300], [1, 1], group, sm_scale=sm_scale)
-            assert_attention_close(got, want)
+            for path in (q4.PATH_DECODE, q4.PATH_PREFILL):
+                got = q4.int4_cache_attention(q, packed, scales, table, lens, group, zeros=zeros, return_lse=True,
+                                              sm_scale=sm_scale, path=path)
+                assert_attention_close(got, want)
 
 
 def test_attention_is_deterministic_and_keeps_nothing():
