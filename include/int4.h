@@ -429,7 +429,7 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * cores: q and the codes exactly (elements of q below 2^-24 of the row's
  * largest to 2^-38 of it), the weights exp(S_j - max) s_j, s_j the value
  * scales, in fp16 after two roundings, each off by at most 2^-11 of the value,
- * or, below 2^-20 s, by 2^-32 s, where s is the largest value scale and lies
+ * or, below 2^-20 s, by 2^-31 s, where s is the largest value scale and lies
  * between 2^-8 and 2^8 (2^-24 s for larger, 2^-40 for smaller ones).
  * INT4_PATH_PREFILL rounds the weight once; with several groups a head it rounds
  * the values too, by 2^-11 of themselves, or 2^-20 of the token's largest scale

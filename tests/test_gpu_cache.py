@@ -304,6 +304,27 @@ def test_attention_tokens_hidden_from_some_rows(path, bad):
 
 
 @pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE, q4.PATH_PREFILL])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("D, group", [(128, 32), (128, 64), (96, 32), (64, 32)])
+def test_attention_one_bad_group(D, group, bad, path):
+    """One group's scale that is not finite: its token's readers and no other row."""
+    q, packed, scales, zeros, table, lens, group = attention_setup(D=D, group=group, lens=(70, 45), ratio=2, affine=False)
+    q = torch.randn((8, 4, D), generator=torch.Generator().manual_seed(3)).cuda().bfloat16()
+    for kv in (0, 1):
+        dirty = scales.clone()
+        dirty[table[0, 68 // 16].long(), kv, :, 68 % 16, -1] = bad  # seen by the last two queries of sequence 0
+        packed[table[0, 68 // 16].long(), kv, :, 68 % 16, -1] = 0x21  # values that are not 0
+        out, lse = q4.int4_cache_attention(q, packed, dirty, table, lens, group, zeros=zeros, return_lse=True, path=path)
+        if kv:
+            assert not torch.isfinite(out[2:4, :, -2:]).any() and torch.isfinite(lse[2:4]).all()
+        else:
+            assert not torch.isfinite(lse[2:4]).any() or bad == math.inf
+        want = attention_ref(q, packed, scales, zeros, table, [70, 45], [4, 4], group)
+        keep = [0, 1, 4, 5, 6, 7]
+        assert_attention_close((out[keep], lse[keep]), tuple(x[keep] for x in want))
+
+
+@pytest.mark.parametrize("path", [q4.PATH_SIMT, q4.PATH_DECODE, q4.PATH_PREFILL])
 def test_attention_unknown_pages_hold_no_tokens(path):
     q, packed, scales, zeros, table, lens, group = attention_setup(lens=(200, 33, 64))
     table[0, 2], table[0, 5], table[2, :] = -7, packed.shape[0], 1 << 30
