@@ -25,10 +25,13 @@
 // value scale the weight, W = 2^x P s rounded to fp16 once (x: a power of two
 // that keeps it in range).  With several groups, the power of two u of the
 // token's largest scale takes the scale's place there, and the elements are
-// (n - z) s / u: values rounded to fp16, keys as the sum of two fp16 numbers, a
-// product each, which hold all of their at most 16 bits (to 2^-20 u, where the
-// scales of a token's groups differ by more than 2^9); the second takes the
-// place of the keys' second stage in shared memory.  S, the maximum and
+// (n - z) s / u: the sum of two fp16 numbers, a product each, which hold all of
+// their at most 16 bits (to 2^-20 u, where the scales of a token's groups differ
+// by more than 2^9); the second takes the place of the second stage in shared
+// memory.  Values for bf16 outputs are rounded to one fp16 number, 2^-11 beside
+// the output's 2^-8; for fp16 outputs that would add half the error that they
+// have (3.0e-4 of the output's norm, 2.4e-4 in two parts; 2048 rows in groups of
+// 32 on 16384 tokens: 322 us and 392 us).  S, the maximum and
 // the sum are fp32; O is fp32 in tensor memory.  Weights are taken relative to a
 // reference that follows the row's maximum only when that has passed it by
 // more than a factor 2^8: a half tile's weights are computed at once under the
@@ -209,6 +212,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                              uint32_t* status) {
   using L = Smem<D>;
   constexpr int kStagesK = GROUPED ? 1 : 2;
+  constexpr bool kExactV = GROUPED && std::is_same<T, __half>::value;  // values in two parts
+  constexpr int kStagesV = kExactV ? 1 : 2;
   constexpr float kNegInf = -__builtin_huge_valf();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -352,9 +357,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       auto o_mma = [&](int m, int stage, int h, bool first) {
         const uint32_t v_lo = v_lo0 + stage * (L::kTile >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ts(lead, tmem + 2 * kTok + m * D, tmem + m * kTok + h * 64 + 8 * k, desc_at(v_lo, h * 8192 + k * 2048), id_o,
-                 first && k == 0 ? 0u : 1u);
+        for (int part = 0; part < (kExactV ? 2 : 1); ++part) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(lead, tmem + 2 * kTok + m * D, tmem + m * kTok + h * 64 + 8 * k,
+                   desc_at(v_lo, part * L::kTile + h * 8192 + k * 2048), id_o, first && part == 0 && k == 0 ? 0u : 1u);
+        }
         commit(lead, bar(bars->o_done[m]));
       };
       int t = 0;  // tiles before this one
@@ -370,14 +378,14 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         for (int i = 0; i < 4; ++i) s_mma(i & 1, t % kStagesK, i >> 1);
         commit(lead, bar(bars->k_empty[t % kStagesK]));
         for (int j = 0; ok && j < n; ++j, ++t) {
-          ok = wait_all(bar(bars->v_full[t & 1]), (t >> 1) & 1u, wc);
+          ok = wait_all(bar(bars->v_full[t % kStagesV]), (t / kStagesV) & 1u, wc);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int m = i & 1, h = i >> 1;
             ok = ok && wait_all(bar(bars->w_full[m][h]), t & 1u, wc);
             if (!ok) break;
             ptx::tc_fence_after();
-            o_mma(m, t & 1, h, j == 0 && h == 0);
+            o_mma(m, t % kStagesV, h, j == 0 && h == 0);
             // Then S into the buffer that the W V before this one has read, one
             // step behind, so that it does not wait for it.
             if (i == 0) {
@@ -395,7 +403,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             }
           }
           if (!ok) break;
-          commit(lead, bar(bars->v_empty[t & 1]));
+          commit(lead, bar(bars->v_empty[t % kStagesV]));
           if (j + 1 == n) commit(lead, bar(bars->o_full));
         }
         if (!ok) break;
@@ -540,11 +548,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           ptx::mbar_arrive(bar(bars->k_full[t % kStagesK]));
         }
         if (j + 1 < n) load(row_next, kx);
-        if (!(ok = wait_all(bar(bars->v_empty[t & 1]), ((t >> 1) & 1u) ^ 1u, wc))) break;
-        store(vx, ptx::smem_u32(smem + L::offV + (t & 1) * L::kTile), v_top, false);
+        if (!(ok = wait_all(bar(bars->v_empty[t % kStagesV]), ((t / kStagesV) & 1u) ^ 1u, wc))) break;
+        store(vx, ptx::smem_u32(smem + L::offV + (t % kStagesV) * L::kTile), v_top, kExactV);
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(bars->v_full[t & 1]));
+        if (lane == 0) ptx::mbar_arrive(bar(bars->v_full[t % kStagesV]));
         if (j + 1 < n) load(row_next < 0 ? row_next : row_next + to_values, vx);
         row = row_next;
         row_next = row_after;

@@ -431,10 +431,10 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * scales, in fp16 after two roundings, each off by at most 2^-11 of the value,
  * or, below 2^-20 s, by 2^-31 s, where s is the largest value scale and lies
  * between 2^-8 and 2^8 (2^-24 s for larger, 2^-40 for smaller ones).
- * INT4_PATH_PREFILL rounds the weight once; with several groups a head it rounds
- * the values too, by 2^-11 of themselves, or 2^-20 of the token's largest scale
- * where that is more, and the keys by at most the latter.  Deterministic for given
- * sizes, lengths and device.
+ * INT4_PATH_PREFILL rounds the weight once; with several groups a head keys and
+ * values are off by at most 2^-20 of the token's largest scale, and values for
+ * bf16 are rounded by 2^-11 of themselves.  Deterministic for given sizes, lengths
+ * and device.
  * NaN or infinity in a query makes its own rows NaN, a value scale that is not
  * finite the outputs (not the lse) of the rows that see its token.
  *
