@@ -43,8 +43,9 @@
 // alone take 250 us, with the hand-overs between S, softmax and W V and a
 // trivial softmax 440 us: each change between the two products drains the pipe
 // for about 300 cycles, and tensor memory has no room for longer products.
-// With groups the expansion bounds it: 8 heads of 128, 2048 rows of one sequence
-// of 16384 tokens take 206 us in one group and 322 us in groups of 32.
+// With groups it is the second products, half as many MMAs again: 8 heads of 128,
+// 2048 rows of one sequence of 16384 tokens take 206 us in one group, 322 us in
+// groups of 32 (392 us with the values in two parts), alike in groups of 64.
 //
 // Inside blocks of 8 elements, keys and queries are stored in the order 0, 4,
 // 1, 5, 2, 6, 3, 7 in which a code word expands pair by pair; O's columns come
