@@ -51,7 +51,7 @@
 // What bounds it.  64 sequences of up to 8192 tokens, 64 query heads of 128 on
 // 8: 75 us for 313 MB, 4.2 TB/s; the slope between two lengths is 6.2 TB/s, and
 // 16 us of set-up, merges and join come on top.  One sequence of 131071 tokens
-// in groups of 32: 46 us for 151 MB, four scales and products to a head beside
+// in groups of 32: 43 us for 151 MB, four scales and products to a head beside
 // the codes.  One sequence of 2048 tokens, 7.5 us: the latency of the set-up (2),
 // the first tile (2), merge and cluster join (2).  More rows to a tile (8
 // queries of 4 heads, 32 sequences of up to 4096 tokens, 55 us): latency of the
