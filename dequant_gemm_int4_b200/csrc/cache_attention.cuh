@@ -87,10 +87,10 @@ struct AttentionSpace {
 };
 
 // Row tile `rt` (rows [rt RT, (rt + 1) RT) of a sequence's query tokens x
-// ratio): the tokens it needs, from lo (a multiple of a warp's tile) to hi,
-// and its steps.
+// ratio): the tokens that its rows see, from first to hi, those that it needs,
+// from lo (first rounded down to a multiple of a warp's tile) on, and its steps.
 struct RowTile {
-  int lo, hi, steps;
+  int lo, first, hi, steps;
   __device__ __forceinline__ void set(const AttentionArgs& a, int len, int count, int rt, int RT) {
     const int step = attention_step(a.cache.head_dim, RT);
     const int r0 = rt * RT, rows = count * a.ratio;
@@ -99,6 +99,7 @@ struct RowTile {
     int lo0, hi0, lo1, hi1;
     a.visible(len - count + i0, len, lo0, hi0);
     a.visible(len - count + i1, len, lo1, hi1);
+    first = lo0;
     lo = lo0 & -(step / kAttnWarps);
     hi = hi1;
     steps = hi > lo ? (hi - lo + step - 1) / step : 0;
@@ -745,10 +746,17 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
               if (!here || tok < s_lo[r + 1] || tok >= s_hi[r + 1]) s[mb][nt][half].y = kNegInf;
             }
             // A value scale that is not finite counts as 0, so that hidden
-            // tokens add nothing; a row that sees one is remembered.
+            // tokens add nothing; a row that sees one is remembered.  So does
+            // that of a token that no row sees (or of a block of tokens that is
+            // not there, whose place holds anything): x_run must not follow it.
+            const int pair = base + mb * 16 + half * 8 + 2 * t;
+            const uint32_t see0 = here && pair >= s_lo[0] && pair < tile.hi ? 0xffffffffu : 0u;
+            const uint32_t see1 = here && pair + 1 >= s_lo[0] && pair + 1 < tile.hi ? 0xffffffffu : 0u;
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-              const uint32_t w = vs[mb][half][i];
+              // The words' first NG halves are the first token's.
+              const uint32_t of0 = (2 * i < NG ? 0xFFFFu : 0u) | (2 * i + 1 < NG ? 0xFFFF0000u : 0u);
+              const uint32_t w = vs[mb][half][i] & ((see0 & of0) | (see1 & ~of0));
               vs[mb][half][i] = ((w & 0x7C00u) != 0x7C00u ? w & 0xFFFFu : 0u) |
                                 ((w & 0x7C000000u) != 0x7C000000u ? w & 0xFFFF0000u : 0u);
               vtop = attn::max_half2(vtop, vs[mb][half][i]);

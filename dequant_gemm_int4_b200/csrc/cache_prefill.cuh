@@ -428,9 +428,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const int64_t page_rows = static_cast<int64_t>(2 * cache.heads) << page_shift;
     const int64_t to_values = static_cast<int64_t>(cache.heads) << page_shift;
     constexpr int kVec = D / 32;  // 16-byte vectors of a row
-    // The row of this thread's token in the tile at `tok`, -1 if there is none.
+    // The row of this thread's token in the tile at `tok`, -1 if there is none
+    // or no row sees it.
     auto find = [&](int tok) -> int64_t {
-      if (tok >= w.tile.hi) return -1;
+      if (tok < w.tile.first || tok >= w.tile.hi) return -1;
       const int id = __ldg(a.page_table + w.b * a.table_stride + (tok >> page_shift));
       if (id < 0 || id >= cache.pages) return -1;
       return id * page_rows + (static_cast<int64_t>(w.h) << page_shift) + (tok & (cache.page_size - 1));

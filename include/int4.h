@@ -410,8 +410,8 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * A query that sees no token gets out = 0 and lse = -infinity.  Rows that
  * belong to no sequence (past q_starts[batch]) are left as they were.
  *
- * Never read: tokens that no query sees, and table entries past a sequence's
- * last token.  Stored NaN or infinity there has no effect.  A table entry that
+ * Without any effect: what is stored for tokens that no query sees, finite or
+ * not, and table entries past a sequence's last token.  A table entry that
  * is negative or at least `pages` holds no tokens (its positions are hidden);
  * kv_lens below 0 counts as 0, above max_pages * page_size as that.
  *
