@@ -316,6 +316,9 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ void sts_u16(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(v)) : "memory");
+}
 __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -703,6 +706,19 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
           }
         }
       }
+      if (base < tile.first || base + TOK > tile.hi || live != (1u << MB) - 1) {
+        // x_run follows the largest value scale of the tile, and W its products:
+        // 0 for the tokens that no row sees, and in the place of a block that is
+        // not there, which holds anything.
+#pragma unroll
+        for (int i = 0; i < TOK; i += 32) {
+          const int tok = base + i + lane;
+          if (((live >> ((i + lane) >> 4)) & 1u) != 0u && tok >= tile.first && tok < tile.hi) continue;
+#pragma unroll
+          for (int c = 0; c < NG; ++c) sts_u16(st + C::kScaleAt + C::kScales + ((i + lane) * NG + c) * 2, 0u);
+        }
+        __syncwarp();
+      }
       // ---- Value scales of tokens 2t, 2t + 1 of each group of 8: NG words
       // hold the two tokens' scales; x_new follows the largest one's exponent.
       uint32_t vs[MB][2][NG];
@@ -746,17 +762,10 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
               if (!here || tok < s_lo[r + 1] || tok >= s_hi[r + 1]) s[mb][nt][half].y = kNegInf;
             }
             // A value scale that is not finite counts as 0, so that hidden
-            // tokens add nothing; a row that sees one is remembered.  So does
-            // that of a token that no row sees (or of a block of tokens that is
-            // not there, whose place holds anything): x_run must not follow it.
-            const int pair = base + mb * 16 + half * 8 + 2 * t;
-            const uint32_t see0 = here && pair >= s_lo[0] && pair < tile.hi ? 0xffffffffu : 0u;
-            const uint32_t see1 = here && pair + 1 >= s_lo[0] && pair + 1 < tile.hi ? 0xffffffffu : 0u;
+            // tokens add nothing; a row that sees one is remembered.
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-              // The words' first NG halves are the first token's.
-              const uint32_t of0 = (2 * i < NG ? 0xFFFFu : 0u) | (2 * i + 1 < NG ? 0xFFFF0000u : 0u);
-              const uint32_t w = vs[mb][half][i] & ((see0 & of0) | (see1 & ~of0));
+              const uint32_t w = vs[mb][half][i];
               vs[mb][half][i] = ((w & 0x7C00u) != 0x7C00u ? w & 0xFFFFu : 0u) |
                                 ((w & 0x7C000000u) != 0x7C000000u ? w & 0xFFFF0000u : 0u);
               vtop = attn::max_half2(vtop, vs[mb][half][i]);
