@@ -522,10 +522,10 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
     uint2 qf[C::kQInRegs ? DB * 2 * NT : 1];
     float2 f[NT], qs1[NT];
     float o[DB][2][NT][4], zo[NG][NT][4];
-    // Per row: the maximum of S / f, -maximum * f (0 before the first token),
-    // and this lane's part of the sum.
+    // Per row: the maximum of S / f, the same negated (0 before the first
+    // token), and this lane's part of the sum.
     float m[NT][2];
-    float2 nmf[NT], l[NT];
+    float2 nm[NT], l[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
 #pragma unroll
         for (int k = 0; k < 4; ++k) zo[gi][nt][k] = 0.0f;
       m[nt][0] = m[nt][1] = kNegInf;
-      nmf[nt] = l[nt] = make_float2(0.0f, 0.0f);
+      nm[nt] = l[nt] = make_float2(0.0f, 0.0f);
     }
     int x_run = 15;  // weights are held 2^x_run fold
     uint32_t bad_rows = 0u;  // rows (two bits an nt) that see a value scale that is not finite: so is their output
@@ -817,8 +817,8 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
           l[nt] = __fmul2_rn(l[nt], al);
           m[nt][0] = mx[nt][0];
           m[nt][1] = mx[nt][1];
-          nmf[nt].x = m[nt][0] == kNegInf ? 0.0f : -m[nt][0] * f[nt].x;
-          nmf[nt].y = m[nt][1] == kNegInf ? 0.0f : -m[nt][1] * f[nt].y;
+          nm[nt].x = m[nt][0] == kNegInf ? 0.0f : -m[nt][0];
+          nm[nt].y = m[nt][1] == kNegInf ? 0.0f : -m[nt][1];
           al.x *= shrink;
           al.y *= shrink;
 #pragma unroll
@@ -832,6 +832,9 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
         }
       }
       // ---- P, its sum, and P 2^x_run in fp16 as the B operand of tokens x rows.
+      // The maximum is taken off before the product with f, so that its own
+      // weight is 1 whatever its size: S f - (m f) in one FMA is off by the
+      // rounding of m f, which passes 1 from |m f| = 2^24 on (and W fp16's range).
       const float xf = __uint_as_float(static_cast<uint32_t>(127 + x_run) << 23);
       const float2 xf2 = make_float2(xf, xf);
       uint32_t pt[MB][NT][2];
@@ -841,7 +844,7 @@ __global__ void __launch_bounds__(kAttnThreads, C::kBlocks)
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            float2 p = __ffma2_rn(s[mb][nt][half], f[nt], nmf[nt]);
+            float2 p = __fmul2_rn(__fadd2_rn(s[mb][nt][half], nm[nt]), f[nt]);
             p.x = ex2(p.x);
             p.y = ex2(p.y);
             l[nt] = __fadd2_rn(l[nt], p);

@@ -68,6 +68,9 @@ constexpr int kTok = 128;      // tokens of a tile
 constexpr int kThreadsP = 512;
 constexpr int kScaleRing = 4;  // tiles of column scales held
 constexpr float kGrow = 8.0f;  // log2 of how far a weight may pass the maximum it is relative to
+// log2 of exponentials up to which the reference is taken off in the same FMA,
+// rounded: by at most 2^-4, for which fp16's range has room beside kGrow.
+constexpr float kNear = 0x1p20f;
 constexpr uint64_t kWaitNs = 250000000ull;  // far above any legitimate wait
 
 struct Bars {
@@ -669,14 +672,15 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             s[i / 2 + 1] = __fmul2_rn(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(k4.z, k4.w));
           }
         };
-        // Their weights W = 2^x P s, and the weights' sum without s.
-        auto weights = [&](int c, const float2 (&s)[8], float2 nmf2, float2& sum, uint32_t (&pw)[8]) {
+        // Their weights W = 2^x P s, and the weights' sum without s.  log2_p: of
+        // a pair of scores, log2 (2^x P).
+        auto weights = [&](int c, const float2 (&s)[8], auto log2_p, float2& sum, uint32_t (&pw)[8]) {
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const float4 v4 = *reinterpret_cast<const float4*>(vc + c + 2 * i);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              float2 p = __ffma2_rn(s[i + k], f2, nmf2);
+              float2 p = log2_p(s[i + k]);
               p.x = attn::ex2(p.x);
               p.y = attn::ex2(p.y);
               sum = __fadd2_rn(sum, p);
@@ -687,7 +691,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         };
         float2 sum = make_float2(0.0f, 0.0f);
         const bool edge = base < all_lo || base + 64 > all_hi || (live.x & live.y) != 0xffffffffu;
-        bool slow = edge || x_new != x_run || (bad.x | bad.y) != 0u;
+        bool slow = edge || x_new != x_run || (bad.x | bad.y) != 0u || __any_sync(0xffffffffu, fabsf(nmf) > kNear);
         if (!slow) {
           // ---- All rows see all tokens: the weights under the reference so
           // far, in registers until it has proved near enough.  One piece of
@@ -708,7 +712,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
               top2[i & 1].x = fmaxf(top2[i & 1].x, s[i].x);
               top2[i & 1].y = fmaxf(top2[i & 1].y, s[i].y);
             }
-            weights(16 * c, s, nmf2, part[c & 1], pw[c]);
+            weights(16 * c, s, [&](float2 y) { return __ffma2_rn(y, f2, nmf2); }, part[c & 1], pw[c]);
           }
           sum = __fadd2_rn(part[0], part[1]);
           const float top = fmaxf(fmaxf(top2[0].x, top2[0].y), fmaxf(top2[1].x, top2[1].y));
@@ -776,14 +780,17 @@ __global__ void __launch_bounds__(kThreadsP, 1)
               }
             }
           }
-          // W follows over the columns of S that have been read.
+          // W follows over the columns of S that have been read.  The reference
+          // is taken off before the product with f: see cache_attention.cuh.
+          const float nr = ref == kNegInf ? 0.0f : -ref;
+          const float2 nr2 = make_float2(nr, nr), x2 = make_float2(static_cast<float>(x_run), static_cast<float>(x_run));
           sum = make_float2(0.0f, 0.0f);
 #pragma unroll 1
           for (int c = 0; c < 64; c += 16) {
             float2 s[8];
             uint32_t y[8];
             load(c, s);
-            weights(c, s, make_float2(nmf, nmf), sum, y);
+            weights(c, s, [&](float2 z) { return __ffma2_rn(__fadd2_rn(z, nr2), f2, x2); }, sum, y);
             tmem_st_32x32b_x8(s_at + c / 2, y);
           }
         }

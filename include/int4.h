@@ -424,7 +424,8 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  *            [0, rows], or NULL (then batch must divide rows).
  * sm_scale   finite.
  *
- * Accuracy: S, the softmax's maximum and sum, and out's sums are fp32.  For
+ * Accuracy: S (of any size that fp32 holds), the softmax's maximum and sum, and
+ * out's sums are fp32.  For
  * fp32 q so are the products.  For bf16 and fp16 q the products run on tensor
  * cores: q and the codes exactly (elements of q below 2^-24 of the row's
  * largest to 2^-38 of it), the weights exp(S_j - max) s_j, s_j the value
