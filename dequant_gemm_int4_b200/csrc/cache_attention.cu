@@ -47,7 +47,10 @@ __global__ void __launch_bounds__(32 * kWarps) attention_any_kernel(
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int d = 2 * (lane + 32 * i) + k;
-      q[2 * i + k] = d < c.head_dim ? Elem<T>::load(qp + d) : 0.0f;
+      const float x = d < c.head_dim ? Elem<T>::load(qp + d) : 0.0f;
+      // Infinity counts as NaN: its products alone could give -infinity for
+      // every score, as if the row saw nothing.
+      q[2 * i + k] = fmaf(x, 0.0f, x);
       o[2 * i + k] = 0.0f;
     }
   }

@@ -619,7 +619,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         }
         int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
         e = e < -100 ? -100 : e;
-        const float scale = sign * __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+        // An infinite element makes the whole row NaN: its products alone could
+        // give -infinity for every score, as if the row saw nothing.
+        const float scale = e == 128 ? __int_as_float(0x7FC00000) : sign * __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
         const uint32_t at = ptx::smem_u32(smem + L::offQ + m * L::kTile) + in_tile * 128;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {

@@ -436,8 +436,11 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * values are off by at most 2^-20 of the token's largest scale, and values for
  * bf16 are rounded by 2^-11 of themselves.  Deterministic for given sizes, lengths
  * and device.
- * NaN or infinity in a query makes its own rows NaN, a value scale that is not
- * finite the outputs (not the lse) of the rows that see its token.
+ * NaN or infinity in a query makes its rows NaN where they see a token.  A value
+ * scale that is not finite makes outputs (not the lse) of the rows that see its
+ * token NaN or infinite, a NaN key scale those rows NaN; an infinite key scale
+ * makes them NaN too, or, in the general kernel, gives that token its scores of
+ * infinity, minus infinity or NaN.
  *
  * `path`: INT4_PATH_AUTO takes a tensor-core kernel where one can run, else the
  * general kernel (INT4_PATH_SIMT).  INT4_PATH_DECODE, for few query rows: bf16 or

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import dequant_gemm_int4_b200 as q4
-from cache_checks import attention_64, made_cache, made_table, token_rows
+from cache_checks import assert_attention_sharp, attention_64, made_cache, made_table, token_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +67,39 @@ def best_scores(q, packed, scales, zeros, table, lens, counts, group, sm_scale):
         gap[at] = best[..., 0] - best[..., 1] if n > 1 else math.inf
         size[at] = sm_scale * x.norm(dim=2) * k_size.norm(dim=2).amax(0).repeat_interleave(ratio)
     return gap.nan_to_num(0.0, math.inf, 0.0), size
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("code", [-3, 0, 5])
+def test_infinite_query_makes_its_row_nan(code, bad, dtype, path):
+    """Whatever the sign of its products: here every key's element is the same,
+    so that all scores of the row are minus infinity, NaN or infinity alike.  A
+    row that sees no token is 0 all the same, and the other rows stay right."""
+    if dtype == torch.float32 and path != q4.PATH_SIMT:
+        pytest.skip("fp32 queries take the general kernel")
+    lens, counts = [300, 0, 2], [5, 2, 4]  # the last sequence's first two rows see nothing
+    table, pages = made_table(lens, 16)
+    packed, scales, _ = made_cache(pages, 16, 2, 64, 64, False)
+    packed[:, 0, :, :, 8] = (packed[:, 0, :, :, 8] & 0x0F) | ((code & 15) << 4)  # element 17
+    q = torch.randn((sum(counts), 4, 64), generator=torch.Generator().manual_seed(2)).cuda().to(dtype)
+    starts = torch.tensor([0, *counts], device="cuda").cumsum(0).int()
+
+    def call():
+        return q4.int4_cache_attention(q, packed, scales, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                       64, q_starts=starts, return_lse=True, path=path)
+    clean, clean_q = call(), q.clone()
+    rows = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    rows[[1, 4, 5, 7, 8, 9, 10], [0, 3, 1, 2, 1, 0, 3]] = True
+    q[:, :, 17].masked_fill_(rows, bad)
+    out, lse = call()
+    empty = torch.isinf(clean[1])
+    assert empty.sum() == 4 * 4
+    assert torch.isnan(out[rows & ~empty]).all() and torch.isnan(lse[rows & ~empty]).all()
+    assert (out[empty] == 0).all() and torch.equal(lse[empty], clean[1][empty])
+    if path == q4.PATH_PREFILL:  # 32 rows move their reference together, so that the others may round anew
+        out, lse = torch.where(rows[..., None], clean[0], out), torch.where(rows, clean[1], lse)
+        assert_attention_sharp((out, lse), attention_64(clean_q, packed, scales, None, table, lens, counts, 64))
+    else:
+        assert torch.equal(out[~rows], clean[0][~rows]) and torch.equal(lse[~rows], clean[1][~rows])
