@@ -85,6 +85,7 @@ struct Cache {
     if (packed.scalar_type() != at::kByte || packed.dim() != 5 || packed.size(1) != 2 ||
         packed.size(4) != (head_dim + 1) / 2)
       value_error("packed must be uint8 [pages, 2, heads, page_size, ceil(head_dim/2)]");
+    if (packed.size(2) < 1 || packed.size(3) < 1) value_error("the cache's heads and page_size must be >= 1");
     const int64_t groups = group >= head_dim ? 1 : (head_dim + group - 1) / group;
     const auto fits = [&](const Tensor& t) {
       return t.dim() == 5 && t.size(0) == packed.size(0) && t.size(1) == 2 && t.size(2) == packed.size(2) &&
