@@ -55,6 +55,22 @@ int64_t integer(PyObject* o, const char* name) {
   return v;
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    type_error(std::string(name) + " must be a truth value");
+  }
+  return v == 1;
+}
+
+// One of the INT4_PATH_* codes, as far as an int32 holds it.
+int32_t path_code(PyObject* o) {
+  const int64_t v = integer(o, "path");
+  if (v < INT32_MIN || v > INT32_MAX) value_error("path must be one of the PATH_* codes");
+  return static_cast<int32_t>(v);
+}
+
 int dtype_code(const Tensor& t) {
   switch (t.scalar_type()) {
     case at::kFloat: return INT4_DTYPE_F32;
@@ -284,10 +300,11 @@ struct Queries {
 PyObject* workspace_size(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 7)) return nullptr;
   return guarded([&]() -> PyObject* {
+    const int32_t path = path_code(a[6]);
     const Queries x(a[0], a[1], a[2], a[3], a[5], integer(a[4], "group"));
     const Place place(x.cache.device);
     size_t bytes = 0;
-    const int rc = x.workspace(static_cast<int32_t>(integer(a[6], "path")), &bytes);
+    const int rc = x.workspace(path, &bytes);
     return PyLong_FromLongLong(rc == INT4_OK ? static_cast<long long>(bytes) : -rc);
   });
 }
@@ -297,6 +314,8 @@ PyObject* workspace_size(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 16)) return nullptr;
   return guarded([&]() -> PyObject* {
+    const bool causal = truth(a[8], "causal"), return_lse = truth(a[11], "return_lse");
+    const int32_t path = path_code(a[14]);
     const Queries x(a[0], a[1], a[2], a[3], a[6], integer(a[5], "group"));
     const Tensor& q = x.q;
     const Cache& cache = x.cache;
@@ -305,7 +324,6 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor* q_starts = a[7] == Py_None ? nullptr : &cache.index(a[7], "q_starts", at::kInt, batch + 1);
     if (q_starts == nullptr && rows > 0 && (batch == 0 || rows % batch != 0))
       value_error("without q_starts, the batch must divide q's rows");
-    const int causal = PyObject_IsTrue(a[8]);
     int64_t window = a[9] == Py_None ? 0 : integer(a[9], "window");
     if (window < 0) value_error("window must be None or >= 0");
     if (window > INT32_MAX) window = INT32_MAX;
@@ -318,8 +336,6 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }
     }
     if (!std::isfinite(static_cast<float>(scale))) value_error("sm_scale must be finite");
-    const bool return_lse = PyObject_IsTrue(a[11]) == 1;
-    const int32_t path = static_cast<int32_t>(integer(a[14], "path"));
 
     const Place place(cache.device);
     Tensor out, lse;
@@ -362,7 +378,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         static_cast<const int32_t*>(x.table.data_ptr()), x.table.stride(0), static_cast<int32_t>(x.table.size(1)),
         static_cast<const int32_t*>(kv_lens.data_ptr()),
         q_starts == nullptr ? nullptr : static_cast<const int32_t*>(q_starts->data_ptr()), static_cast<int32_t>(batch),
-        causal, static_cast<int32_t>(window), static_cast<float>(scale), out.data_ptr(),
+        causal ? 1 : 0, static_cast<int32_t>(window), static_cast<float>(scale), out.data_ptr(),
         lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, path, workspace, bytes, place.stream);
     if (rc != INT4_OK) return PyLong_FromLong(rc);
     PyObject* py_out = a[12] == Py_None ? THPVariable_Wrap(std::move(out)) : Py_NewRef(a[12]);

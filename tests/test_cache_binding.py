@@ -27,3 +27,20 @@ def test_a_cache_of_no_heads_or_empty_pages(kw):
                  lambda: q4.int4_cache_write(k, k, packed, scales, slots, 32)):
         with pytest.raises(ValueError, match="heads and page_size"):
             call()
+
+
+@pytest.mark.parametrize("name", ["causal", "return_lse"])
+@pytest.mark.parametrize("value", [torch.tensor([True, False]), np.array([1, 0])])
+def test_flags_that_are_no_truth_value(name, value):
+    q, packed, scales, table, lens = tensors()
+    with pytest.raises(TypeError, match=name):
+        q4.int4_cache_attention(q, packed, scales, table, lens, 32, **{name: value})
+
+
+@pytest.mark.parametrize("path", [1 << 32, -(1 << 40), (1 << 32) + q4.PATH_DECODE, 2.0, None])
+def test_paths_out_of_range(path):
+    q, packed, scales, table, lens = tensors()
+    for call in (q4.int4_cache_attention, q4.cache_attention_workspace_size):
+        args = (q, packed, scales, table) + ((lens,) if call is q4.int4_cache_attention else ())
+        with pytest.raises((ValueError, TypeError), match="path must"):
+            call(*args, 32, path=path)
