@@ -56,11 +56,13 @@ __global__ void __launch_bounds__(32 * kWarps) attention_any_kernel(
   }
   float m = __int_as_float(0xFF800000), l = 0.0f;  // in units of log2
   const float to_log2 = a.sm_scale * kLog2e;
-  for (int j = lo + warp; j < hi; j += kWarps) {
-    const int64_t page = __ldg(a.page_table + b * a.table_stride + j / c.page_size);
+  // Unsigned: hi may be 2^31 - 1, and the last step goes past it.
+  const uint32_t page_size = c.page_size;
+  for (uint32_t j = lo + warp; j < static_cast<uint32_t>(hi); j += kWarps) {
+    const int64_t page = __ldg(a.page_table + b * a.table_stride + j / page_size);
     if (page < 0 || page >= c.pages) continue;  // no such page: its tokens are not there
-    const int64_t kr = c.row(page, 0, h, j % c.page_size);
-    const int64_t vr = c.row(page, 1, h, j % c.page_size);
+    const int64_t kr = c.row(page, 0, h, j % page_size);
+    const int64_t vr = c.row(page, 1, h, j % page_size);
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < BYTES; ++i) {
