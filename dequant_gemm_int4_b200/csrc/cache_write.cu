@@ -270,14 +270,14 @@ template <typename T, bool ASYM>
 __global__ void __launch_bounds__(256) cache_write_any_kernel(const __grid_constant__ WriteArgs a) {
   const CacheView& c = a.cache;
   const int lane = threadIdx.x & 31;
-  const int rows = 2 * c.heads;
+  const int64_t rows = 2LL * c.heads;
   const int64_t total = a.tokens * rows;
   const int64_t step = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
   for (int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; w < total; w += step) {
     const int64_t t = w / rows;
-    const int row = static_cast<int>(w - t * rows);
-    const int kv = row >= c.heads ? 1 : 0;
-    const int h = row - kv * c.heads;
+    const uint32_t row = static_cast<uint32_t>(w - t * rows);  // below 2^32: heads are below 2^31
+    const int kv = row >= static_cast<uint32_t>(c.heads) ? 1 : 0;
+    const int h = static_cast<int>(row - kv * static_cast<uint32_t>(c.heads));
     const int64_t slot = __ldg(a.slots + t);
     if (slot < 0 || slot >= c.pages * c.page_size) continue;
     const T* x = static_cast<const T*>(a.src[kv]) + t * a.token_stride[kv] + h * a.head_stride[kv];
@@ -401,10 +401,10 @@ __global__ void __launch_bounds__(256) cache_read_any_kernel(const __grid_consta
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
     const int64_t t = i / per_token;
     const int64_t in_token = i - t * per_token;
-    const int row = static_cast<int>(in_token / c.row_bytes);
+    const uint32_t row = static_cast<uint32_t>(in_token / c.row_bytes);  // as above
     const int b = static_cast<int>(in_token - static_cast<int64_t>(row) * c.row_bytes);
-    const int kv = row >= c.heads ? 1 : 0;
-    const int h = row - kv * c.heads;
+    const int kv = row >= static_cast<uint32_t>(c.heads) ? 1 : 0;
+    const int h = static_cast<int>(row - kv * static_cast<uint32_t>(c.heads));
     const int64_t slot = __ldg(a.slots + t);
     const bool live = slot >= 0 && slot < c.pages * c.page_size;
     const int64_t at = live ? c.row(slot / c.page_size, kv, h, slot % c.page_size) : 0;

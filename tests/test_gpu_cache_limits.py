@@ -25,3 +25,23 @@ def test_general_kernel_at_the_longest_sequence(n):
     want = call(table[:, -1:], n - 2047 * S)
     # Warps take tokens in turn from the first one seen on, in both calls alike.
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("affine", [False, True])
+def test_more_heads_than_2_to_30(affine):
+    """Rows of a token (keys and values of all heads) counted beyond 2^31."""
+    H, D = 2 ** 30 + 5, 1
+    cache = q4.Int4KVCache(1, 1, H, D, scheme="affine" if affine else "symmetric")
+    x = torch.zeros((2, 1, H, D), dtype=torch.float16, device="cuda")
+    at = torch.tensor([0, 1, 7, 2 ** 29, 2 ** 30 - 1, 2 ** 30, H - 2, H - 1], device="cuda")
+    x[:, 0, at, 0] = torch.arange(1, 17, device="cuda").half().view(2, 8) * 0.07
+    slots = torch.zeros(1, dtype=torch.int64, device="cuda")
+    cache.write(x[0], x[1], slots)
+    got = cache.read(slots, torch.float16)
+    small = q4.Int4KVCache(1, 1, 8, D, scheme="affine" if affine else "symmetric")
+    small.write(x[0][:, at], x[1][:, at], slots)
+    for i, (a, b) in enumerate(zip(got, small.read(slots, torch.float16))):
+        assert torch.equal(a[:, at], b) and (b != 0).any() != affine
+        assert a.count_nonzero() == b.count_nonzero()
+        assert torch.equal(cache.packed[0, i, at, 0], small.packed[0, i, :, 0])
+        assert torch.equal(cache.scales[0, i, at, 0], small.scales[0, i, :, 0])
