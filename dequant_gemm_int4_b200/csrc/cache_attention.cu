@@ -160,22 +160,33 @@ cudaError_t launch_cache_attention_any(const AttentionArgs& a, DType t, cudaStre
   }
 }
 
+namespace {
+
 // The tensor-core kernels take 16-bit queries, heads of 64, 96, 128 or 256
 // elements in groups of 32, 64, 128 or the whole head, and pages of a power
 // of two of tokens, at least 16 (a block of 16 tokens then lies in one page).
 // Token positions are 32-bit there, with room for a look-ahead of 16 steps.
-// All counts of steps are 32-bit too.
-bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out, int64_t rows, int64_t batch,
-                                   int ratio, int64_t max_pages) {
+// So are all counts of steps, of 128 tokens or more for each `row_tile` rows
+// of a head.
+bool mma_supported(const CacheView& c, DType t, const void* out, int64_t rows, int64_t batch, int ratio,
+                   int64_t max_pages, int row_tile) {
   const int d = c.head_dim, g = c.group;
   const bool shape = (d == 64 || d == 96 || d == 128 || d == 256) && d % g == 0 &&
                      (g == 32 || g == d || (d != 96 && (g == 64 || g == 128)));
   const bool pages = c.page_size >= 16 && (c.page_size & (c.page_size - 1)) == 0 &&
                      max_pages * c.page_size <= (1LL << 30) &&
-                     static_cast<double>(c.heads) * (static_cast<double>(rows) * ratio / 8 + batch) *
-                             (static_cast<double>(max_pages) * c.page_size / 128 + 1) < 0x40000000;
+                     static_cast<double>(c.heads) * (static_cast<double>(rows) * ratio / row_tile + batch) *
+                             (static_cast<double>(max_pages) * c.page_size / 128 + 1) < 0x7FFF0000;
   return t != DType::F32 && shape && pages && multiple_of(c.packed, 16) && multiple_of(c.scales, 16) &&
          multiple_of(c.zeros, 16) && multiple_of(out, 8);
+}
+
+}  // namespace
+
+bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out, int64_t rows, int64_t batch,
+                                   int ratio, int64_t max_pages) {
+  const int rt = batch > 0 ? attention_row_tile(c.head_dim, rows, batch, ratio) : 8;
+  return mma_supported(c, t, out, rows, batch, ratio, max_pages, rt);
 }
 
 // The tcgen05 kernel takes heads of 64, 96 or 128 elements in one group or in
@@ -183,7 +194,7 @@ bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out,
 bool cache_prefill_supported(const CacheView& c, DType t, const void* out, int64_t rows, int64_t batch, int ratio,
                              int64_t max_pages) {
   return (c.head_dim == 64 || c.head_dim == 96 || c.head_dim == 128) && multiple_of(out, 16) &&
-         cache_attention_mma_supported(c, t, out, rows, batch, ratio, max_pages);
+         mma_supported(c, t, out, rows, batch, ratio, max_pages, kPrefillRowTile);
 }
 
 size_t cache_prefill_workspace(const CacheView& c, int64_t batch) {

@@ -446,10 +446,11 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * general kernel (INT4_PATH_SIMT).  INT4_PATH_DECODE, for few query rows: bf16 or
  * fp16 q, head_dim 64, 96, 128 or 256 in groups of 32, 64, 128 or head_dim (96:
  * 32 or 96), page_size a power of two from 16 on, max_pages * page_size <= 2^30
- * (and steps of 128 tokens over all heads below 2^30), packed, scales and zeros
- * 16-byte and out 8-byte aligned.  INT4_PATH_PREFILL, for many: of those,
- * head_dim 64, 96 or 128, out 16-byte aligned.  A forced path that
- * cannot run the call returns INT4_ERR_UNSUPPORTED.
+ * (and the table's steps of 128 tokens, for each tile of 8, 16 or 32 rows of
+ * every head, below 2^31), packed, scales and zeros 16-byte and out 8-byte
+ * aligned.  INT4_PATH_PREFILL, for many: of those, with tiles of 256 rows,
+ * head_dim 64, 96 or 128, out 16-byte aligned.  A forced path that cannot run
+ * the call returns INT4_ERR_UNSUPPORTED.
  *
  * workspace: at least int4_cache_attention_workspace_size bytes (else
  * INT4_ERR_ARG, nothing launched), 256-byte aligned, of any content; NULL with

@@ -1,0 +1,37 @@
+"""Which kernel takes a call, asked of the C entry on the host: calls that the
+tensor-core kernels can run do not fall to the general one.  No GPU needed."""
+
+import ctypes
+
+import pytest
+
+import dequant_gemm_int4_b200 as q4
+from dequant_gemm_int4_b200 import build as q4build
+from test_cache_host import cache
+
+
+@pytest.fixture(scope="module")
+def L():
+    q4build.build()
+    return q4.lib()
+
+
+@pytest.mark.parametrize("rows, q_heads, tokens, path", [
+    (131072, 32, 262144, q4.PATH_AUTO), (131072, 32, 262144, q4.PATH_PREFILL),
+    (262144, 64, 262144, q4.PATH_AUTO), (1 << 20, 32, 1 << 20, q4.PATH_PREFILL),
+    (131072, 32, 1 << 20, q4.PATH_DECODE),
+])
+def test_large_prompts_take_a_tensor_core_kernel(L, rows, q_heads, tokens, path):
+    size = ctypes.c_size_t(0)
+    c = cache(pages=tokens // 64, page_size=64, heads=8, head_dim=128, group=128)
+    rc = L.int4_cache_attention_workspace_size(c, 1, rows, q_heads, 1, tokens // 64, path, ctypes.byref(size))
+    assert rc == q4.OK, L.int4_last_error()
+    assert size.value > 0  # the general kernel needs none
+
+
+def test_more_steps_than_32_bits_are_refused(L):
+    size = ctypes.c_size_t(0)
+    c = cache(pages=1 << 20, page_size=1024, heads=8, head_dim=128, group=128)
+    for path in (q4.PATH_DECODE, q4.PATH_PREFILL):
+        assert L.int4_cache_attention_workspace_size(c, 1, 1 << 24, 64, 1, 1 << 20, path,
+                                                     ctypes.byref(size)) == q4.ERR_UNSUPPORTED

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import dequant_gemm_int4_b200 as q4
-from cache_checks import made_cache
+from cache_checks import assert_attention_sharp, attention_64, made_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,21 @@ def test_more_heads_than_2_to_30(affine):
         assert a.count_nonzero() == b.count_nonzero()
         assert torch.equal(cache.packed[0, i, at, 0], small.packed[0, i, :, 0])
         assert torch.equal(cache.scales[0, i, at, 0], small.scales[0, i, :, 0])
+
+
+def test_a_large_prompt_through_a_window():
+    """131072 rows on 262144 tokens: many steps in the table, few in the window."""
+    rows, n, D, H, S = 131072, 262144, 64, 2, 128
+    packed, scales, zeros = made_cache(n // S, S, H, D, 64, False)
+    table = torch.randperm(n // S, generator=torch.Generator().manual_seed(1)).int().cuda()[None]
+    q = torch.randn((rows, 32, D), generator=torch.Generator(device="cuda").manual_seed(0), device="cuda").bfloat16()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out, lse = q4.int4_cache_attention(q, packed, scales, table, lens, 64, window=100, return_lse=True)
+    for first in (0, 70000, rows - 50):  # 50 rows at a time, their last token the sequence's last
+        part = slice(first, first + 50)
+        length = n - rows + first + 50
+        first_page = max(0, length - 200) // S  # what the window does not reach left out
+        want = attention_64(q[part], packed, scales, zeros, table[:, first_page:], [length - first_page * S], [50], 64,
+                            window=100)
+        assert_attention_sharp((out[part], lse[part]), want)
+    assert q4.device_status() == q4.OK
