@@ -158,3 +158,37 @@ def test_many_rows_past_four_gigabytes():
         path=q4.PATH_PREFILL)
     for a, b in zip(call((packed, scales), at), call(small, [0, 1, 2, 3])):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("affine", [False, True])
+@pytest.mark.parametrize("D, group, ratio", [(64, 64, 8), (128, 128, 3), (128, 32, 8), (96, 96, 1), (256, 256, 4),
+                                             (256, 32, 8)])
+@pytest.mark.parametrize("window", [None, 100])
+def test_few_rows_kernel_on_many_row_tiles(D, group, ratio, window, affine):
+    """Several row tiles a sequence, split items among them, rows that see nothing, a mixed batch."""
+    run(2, ratio, D, group, 32, [3000, 40, 0, 700, 1500], [333, 60, 7, 1, 90], "f16" if affine else "bf16",
+        q4.PATH_DECODE, affine=affine, window=window)
+    run(2, ratio, D, group, 64, [900] + [500] * 40, [200] + [1] * 40, "bf16", q4.PATH_DECODE, affine=affine,
+        window=window)
+
+
+@pytest.mark.parametrize("D, counts", [(256, 1), (128, 1), (64, 4)])
+def test_the_few_rows_kernel_is_linear_in_its_rows(D, counts):
+    """Four times the rows, each of which sees 64 tokens, in less than eight times the time."""
+    times = []
+    for rows in (4096, 16384):
+        table, pages = made_table([rows], 64)
+        packed, scales, _ = made_cache(pages, 64, 4, D, D, False)
+        q = torch.randn((rows, 32, D), device="cuda").bfloat16()
+        starts = torch.tensor([0] * counts + [rows], dtype=torch.int32, device="cuda")
+        table, lens = table.repeat(counts, 1), torch.full((counts,), rows, dtype=torch.int32, device="cuda")
+        best = 1e30
+        for _ in range(5):
+            begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            begin.record()
+            q4.int4_cache_attention(q, packed, scales, table, lens, D, q_starts=starts, window=64, path=q4.PATH_DECODE)
+            end.record()
+            torch.cuda.synchronize()
+            best = min(best, begin.elapsed_time(end))
+        times.append(best)
+    assert times[1] < 8 * times[0], times
