@@ -63,3 +63,30 @@ def test_a_large_prompt_through_a_window():
                             window=100)
         assert_attention_sharp((out[part], lse[part]), want)
     assert q4.device_status() == q4.OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D, group", [(128, 32), (64, 64), (80, 48), (33, 7)])
+def test_write_codes_as_the_weight_quantizers_at_any_size(D, group, dtype):
+    """The cache codes its rows in arithmetic of its own: the same bits as
+    quantize_int4 and quantize_int4_affine from fp16's subnormal scales to its
+    largest, for groups far from 0, constant groups and single large elements."""
+    T, H = 2048, 4
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    x = torch.randn((T, H, D), generator=gen, device="cuda")
+    most = 14 if dtype == torch.float16 else 17
+    x *= torch.exp2(torch.randint(-30, most, (T, H, 1), generator=gen, device="cuda").float())
+    x[::5] += x[::5].abs().amax(-1, keepdim=True) * torch.exp2(torch.randint(-8, 2 if most == 14 else 9, (len(x[::5]), H, 1),
+                                                                           generator=gen, device="cuda").float())
+    x[1::7, :, ::3] = 0.5
+    x[2::11, :, D // 2] *= 100.0
+    x = x.clamp(-6e4, 6e4) if dtype == torch.float16 else x.clamp(-4e5, 4e5)
+    x = x.to(dtype)
+    for scheme, f in (("symmetric", q4.quantize_int4), ("affine", q4.quantize_int4_affine)):
+        y = x if scheme == "symmetric" else x.clamp(-2e5, 2e5)
+        cache = q4.Int4KVCache(T // 64, 64, H, D, group=group, scheme=scheme)
+        cache.write(y, y.flip(0), torch.arange(T, device="cuda"))
+        for i, z in enumerate((y, y.flip(0))):
+            for got, ref in zip(cache.buffers(), f(z.reshape(-1, D).contiguous(), group)[:-1]):
+                got = got[:, i].transpose(1, 2).reshape(T * H, -1)
+                assert torch.equal(got.view(torch.uint8), ref.view(torch.uint8))
