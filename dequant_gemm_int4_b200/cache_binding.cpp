@@ -258,6 +258,8 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       need_dense(out[i], "out");
       cache.on(out[i], "out");
     }
+    const char* const at[2] = {static_cast<const char*>(out[0].data_ptr()), static_cast<const char*>(out[1].data_ptr())};
+    if (at[0] < at[1] + out[1].nbytes() && at[1] < at[0] + out[0].nbytes()) value_error("out's two tensors overlap");
     const int rc = p_read(&cache.c, static_cast<const int64_t*>(slots.data_ptr()), slots.size(0), out[0].data_ptr(),
                           out[1].data_ptr(), static_cast<int32_t>(code), place.stream);
     if (rc != INT4_OK) return PyLong_FromLong(rc);

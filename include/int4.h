@@ -372,7 +372,9 @@ typedef struct {
  * slots    [tokens] int64 device input, 8-byte aligned.  A token whose slot is
  *          negative or at least pages * page_size (padding) is not written.
  *          The other slots must be distinct: two tokens in one slot race.
- * Bit-exact.  Precondition: k and v are finite (else unspecified codes).
+ * Bit-exact.  Precondition: k and v are finite (else unspecified codes), in the
+ * affine scheme with int4_quantize_affine's range in every group.  They do not
+ * lie in the cache.
  */
 int int4_cache_write(const int4_cache* cache, const void* k, int64_t k_token_stride,
                      int64_t k_head_stride, const void* v, int64_t v_token_stride,
@@ -386,6 +388,7 @@ int int4_cache_write(const int4_cache* cache, const void* k, int64_t k_token_str
  *          to their element size: q s, or (q - z) s, rounded once, to nearest
  *          even (int4_dequantize's rule).  Bit-exact.  A token whose slot is
  *          negative or at least pages * page_size reads as zeros.
+ *          k and v do not overlap one another, the cache or the slots.
  * slots    [tokens] int64 device input, 8-byte aligned; a slot may occur
  *          several times.
  */
@@ -418,7 +421,8 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * q          [rows, q_heads, head_dim] of `dtype`, aligned to its element size;
  *            strides in elements as for int4_cache_write.
  * out        [rows, q_heads, head_dim] dense, of `dtype`.
- * lse        [rows, q_heads] fp32, or NULL.
+ * lse        [rows, q_heads] fp32, or NULL.  Neither out nor lse overlaps an
+ *            input, the workspace or the other.
  * page_table [batch, max_pages] int32, rows `table_stride` elements apart.
  * kv_lens    [batch] int32.  q_starts [batch + 1] int32, non-decreasing, within
  *            [0, rows], or NULL (then batch must divide rows).

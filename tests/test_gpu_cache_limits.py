@@ -90,3 +90,17 @@ def test_write_codes_as_the_weight_quantizers_at_any_size(D, group, dtype):
             for got, ref in zip(cache.buffers(), f(z.reshape(-1, D).contiguous(), group)[:-1]):
                 got = got[:, i].transpose(1, 2).reshape(T * H, -1)
                 assert torch.equal(got.view(torch.uint8), ref.view(torch.uint8))
+
+
+def test_read_refuses_outputs_that_overlap():
+    """The keys' and the values' rows would be written over one another."""
+    cache = q4.Int4KVCache(2, 16, 2, 64)
+    slots = torch.arange(8, device="cuda")
+    both = torch.empty((24, 2, 64), dtype=torch.bfloat16, device="cuda")
+    args = (cache.packed, cache.scales, slots, 64, 64, torch.bfloat16)
+    for k, v in ((both[:8], both[:8]), (both[:8], both[4:12]), (both[15:23], both[8:16])):
+        with pytest.raises(ValueError, match="overlap"):
+            q4.int4_cache_read(*args, out=(k, v))
+    assert q4.int4_cache_read(*args, out=(both[:8], both[8:16]))[1].shape == (8, 2, 64)
+    none = both[:0]
+    q4.int4_cache_read(cache.packed, cache.scales, slots[:0], 64, 64, torch.bfloat16, out=(none, none))
