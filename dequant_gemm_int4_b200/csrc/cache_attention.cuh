@@ -9,7 +9,7 @@
 //   O^T += V^T P^T       mma.m16n8k16, head elements x query rows
 // The codes enter the products as they are: a nibble n (offset to 0..15) in
 // the low bits of a half is the fp16 subnormal n 2^-24, which the tensor core
-// multiplies exactly, so expanding 8 codes takes a shift and four bitwise
+// takes as it is, so expanding 8 codes takes a shift and four bitwise
 // operations and no arithmetic.  The second nibble of a byte stays four bits
 // up and counts 16-fold; the query's element (or the output row) is divided
 // by 16 instead, exactly.  With z the zero point (8 in the symmetric scheme,
@@ -23,11 +23,18 @@
 // smaller than that one, whose error stays below 2^-38 of it.  S, the
 // softmax's maximum and sum and O are fp32.  w_t is rounded to fp16 twice
 // (each by at most 2^-11 of itself): p_t, taken by a power of two that follows
-// the largest value scale so far, and its product with s_t.  A product with
-// that scale lies below 2^15, so weights keep their full precision down to
-// 2^-20 of the largest and in half the fp16 range below it some of it.  With
-// fp32 products the second rounding would go, and a conversion and two
-// multiplications for each weight would come.
+// the largest value scale so far (of tokens that some row sees), and its product
+// with s_t.  A product with that scale lies below 2^15, so weights keep their
+// full precision down to 2^-20 of the largest and in half the fp16 range below
+// it some of it.  With fp32 products the second rounding would go, and a
+// conversion and two multiplications for each weight would come.
+// The tensor core aligns the terms of a step by their operands' exponents, where
+// a subnormal counts as 2^-14, and cuts them off about 25 bits below the
+// largest: the sums over n and over z keep 15 bits or more of sum_t p_t s_t z_t
+// (an output whose values cancel came out 3.5e-5 of that off; 2.6e-4 is what
+// the weights' roundings leave of an output's norm), S about 20 of its terms'
+// (lse: 3e-6 to 7e-6 at scores near 10).  Codes two bits up or more (a shift more
+// for each word of values) brought the first to 9e-6 and cost 1 to 3 %.
 //
 // Layout.  One warp takes 64 tokens at a time (32, for 16 or 32 rows and for
 // heads of 256: the scores fill the registers): their key and value rows are

@@ -436,10 +436,12 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * scales, in fp16 after two roundings, each off by at most 2^-11 of the value,
  * or, below 2^-20 s, by 2^-31 s, where s is the largest value scale and lies
  * between 2^-8 and 2^8 (2^-24 s for larger, 2^-40 for smaller ones).
- * INT4_PATH_PREFILL rounds the weight once; with several groups a head keys and
- * values are off by at most 2^-20 of the token's largest scale, and values for
- * bf16 are rounded by 2^-11 of themselves.  Deterministic for given sizes, lengths
- * and device.
+ * INT4_PATH_DECODE sums the codes and the zero points z (8 in the symmetric
+ * scheme) apart, and its outputs are off by up to 2^-13 of sum_j p_j s_j z_j too,
+ * p_j = exp(S_j - lse).  INT4_PATH_PREFILL rounds the weight once; with several
+ * groups a head keys and values are off by at most 2^-20 of the token's largest
+ * scale, and values for bf16 are rounded by 2^-11 of themselves.  Deterministic
+ * for given sizes, lengths and device.
  * NaN or infinity in a query makes its rows NaN where they see a token.  A value
  * scale that is not finite makes outputs (not the lse) of the rows that see its
  * token NaN or infinite, a NaN key scale those rows NaN; an infinite key scale
