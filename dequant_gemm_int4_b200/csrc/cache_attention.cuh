@@ -33,8 +33,9 @@
 // largest: the sums over n and over z keep 15 bits or more of sum_t p_t s_t z_t
 // (an output whose values cancel came out 3.5e-5 of that off; 2.6e-4 is what
 // the weights' roundings leave of an output's norm), S about 20 of its terms'
-// (lse: 3e-6 to 7e-6 at scores near 10).  Codes two bits up or more (a shift more
-// for each word of values) brought the first to 9e-6 and cost 1 to 3 %.
+// (lse: 3e-6 to 7e-6 at scores near 10).  All codes moved up to bit 6 (three
+// shifts more for each word of values) brought the first below 9e-6 and cost 3
+// to 5 % of the decoding cases: not taken, the weights' roundings being larger.
 //
 // Layout.  One warp takes 64 tokens at a time (32, for 16 or 32 rows and for
 // heads of 256: the scores fill the registers): their key and value rows are
@@ -55,14 +56,15 @@
 // through each other's shared memory, and the second kernel is saved (one
 // sequence of 2048 tokens, 32 query heads on 8: 8.9 us with it, 7.2 without).
 //
-// What bounds it.  64 sequences of up to 8192 tokens, 64 query heads of 128 on
-// 8: 75 us for 313 MB, 4.2 TB/s; the slope between two lengths is 6.2 TB/s, and
-// 16 us of set-up, merges and join come on top.  One sequence of 131071 tokens
-// in groups of 32: 43 us for 151 MB, four scales and products to a head beside
-// the codes.  One sequence of 2048 tokens, 7.5 us: the latency of the set-up (2),
-// the first tile (2), merge and cluster join (2).  More rows to a tile (8
-// queries of 4 heads, 32 sequences of up to 4096 tokens, 55 us): latency of the
-// products and the softmax at three warps a scheduler.
+// What bounds it (times in a captured graph).  64 sequences of up to 8192 tokens,
+// 64 query heads of 128 on 8: 75 us for 313 MB, 4.2 TB/s; the slope between two
+// lengths is 6.2 TB/s, and 16 us of set-up, merges and join come on top.  One
+// sequence of 131071 tokens in groups of 32: 42 us for 151 MB, four scales and
+// products to a head beside the codes.  One sequence of 2048 tokens, 7.2 us: the
+// latency of the set-up (2), the first tile (2), merge and cluster join (2).  More
+// rows to a tile (8 queries of 4 heads, 32 sequences of up to 4096 tokens, 53 us):
+// latency of the products and the softmax at three warps a scheduler (issue slots
+// 49 % taken, tensor pipe 31 %).
 #pragma once
 
 #include <atomic>
@@ -1333,10 +1335,19 @@ __global__ void __launch_bounds__(256)
 
 // Query rows of a tile, by the rows of an average sequence (query tokens times
 // ratio): 8 for up to 8; else 32 where an even number of tiles of 16 holds them
-// and 16 where an odd one does (32 sequences of 4096 tokens, 8 heads of 128:
-// 32 rows 94 us as one tile, 101 us as two; 48 rows 169 us as two tiles of 32,
-// 143 us as three of 16); 16 for 256 elements, where the accumulators of 32
-// rows do not fit in registers.
+// and 16 where an odd one does; 16 for 256 elements, where the accumulators of
+// 32 rows do not fit in registers.  32 sequences of 4096 tokens, 8 heads, in us
+// as tiles of 32 / of 16 rows:
+//   rows                  32          48          64          96
+//   128, one group      98 / 105   169 / 144   173 / 185   244 / 266
+//   128, groups of 64  112 / 124   199 / 176   201 / 226   289 / 335
+//   96, one group       83 / 90    141 / 122   145 / 157   205 / 225
+//   64, one group       74 / 73    131 / 98    133 / 126   180 / 180
+//   128, groups of 32  196 / 153   362 / 223   369 / 288   538 / 426
+//   64, groups of 32   106 / 79    182 / 108   187 / 138   262 / 197
+// The last two, whose tiles of 32 rows spill registers (up to 800 bytes a
+// thread), would be better off with 16 throughout; the rule does not look at the
+// groups yet.
 inline int attention_row_tile(int head_dim, int64_t rows, int64_t batch, int ratio) {
   const int64_t r = (rows * ratio + batch - 1) / batch;
   if (r <= 8) return 8;

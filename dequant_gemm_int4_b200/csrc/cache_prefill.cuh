@@ -31,7 +31,7 @@
 // memory.  Values for bf16 outputs are rounded to one fp16 number, 2^-11 beside
 // the output's 2^-8; for fp16 outputs that would add half the error that they
 // have (3.0e-4 of the output's norm, 2.4e-4 in two parts; 2048 rows in groups of
-// 32 on 16384 tokens: 322 us and 392 us).  S, the maximum and
+// 32 on 16384 tokens: 327 us and 401 us).  S, the maximum and
 // the sum are fp32; O is fp32 in tensor memory.  Weights are taken relative to a
 // reference that follows the row's maximum only when that has passed it by
 // more than a factor 2^8: a half tile's weights are computed at once under the
@@ -39,13 +39,14 @@
 // does not see all tokens, with the maximum first.
 //
 // What bounds it.  1789 queries of two prompts on 8192 and 6757 tokens, 64 heads
-// of 128 on 8: 577 us, of 256 us at the tensor pipe's measured rate.  The MMAs
-// alone take 250 us, with the hand-overs between S, softmax and W V and a
-// trivial softmax 440 us: each change between the two products drains the pipe
+// of 128 on 8: 580 us, of 256 us at the tensor pipe's measured rate (the pipe is
+// active in 37 % of the cycles).  Copies of the kernel that leave parts out took
+// 250 us with the MMAs alone and 440 us with the hand-overs between S, softmax and
+// W V and a trivial softmax: each change between the two products drains the pipe
 // for about 300 cycles, and tensor memory has no room for longer products.
 // With groups it is the second products, half as many MMAs again: 8 heads of 128,
-// 2048 rows of one sequence of 16384 tokens take 206 us in one group, 322 us in
-// groups of 32 (392 us with the values in two parts), alike in groups of 64.
+// 2048 rows of one sequence of 16384 tokens take 265 us in one group, 327 us in
+// groups of 32 (401 us with the values in two parts), alike in groups of 64.
 //
 // Inside blocks of 8 elements, keys and queries are stored in the order 0, 4,
 // 1, 5, 2, 6, 3, 7 in which a code word expands pair by pair; O's columns come
