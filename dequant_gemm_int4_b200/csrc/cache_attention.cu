@@ -185,7 +185,7 @@ bool mma_supported(const CacheView& c, DType t, const void* out, int64_t rows, i
 
 bool cache_attention_mma_supported(const CacheView& c, DType t, const void* out, int64_t rows, int64_t batch,
                                    int ratio, int64_t max_pages) {
-  const int rt = batch > 0 ? attention_row_tile(c.head_dim, rows, batch, ratio) : 8;
+  const int rt = batch > 0 ? attention_row_tile(c.head_dim, c.group, rows, batch, ratio) : 8;
   return mma_supported(c, t, out, rows, batch, ratio, max_pages, rt);
 }
 
@@ -202,7 +202,7 @@ size_t cache_prefill_workspace(const CacheView& c, int64_t batch) {
 }
 
 size_t cache_attention_mma_workspace(const CacheView& c, int64_t rows, int64_t batch, int ratio) {
-  const int rt = attention_row_tile(c.head_dim, rows, batch, ratio);
+  const int rt = attention_row_tile(c.head_dim, c.group, rows, batch, ratio);
   const bool asym = c.zeros != nullptr;
   int blocks = 0;
   switch (c.head_dim) {
@@ -223,7 +223,7 @@ cudaError_t launch_cache_prefill(const AttentionArgs& a, DType t, void* workspac
 }
 
 cudaError_t launch_cache_attention_mma(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream) {
-  const int rt = attention_row_tile(a.cache.head_dim, a.rows, a.batch, a.ratio);
+  const int rt = attention_row_tile(a.cache.head_dim, a.cache.group, a.rows, a.batch, a.ratio);
   switch (a.cache.head_dim) {
     case 64: return launch_cache_attention_64(a, t, rt, workspace, stream);
     case 96: return launch_cache_attention_96(a, t, rt, workspace, stream);

@@ -1335,23 +1335,25 @@ __global__ void __launch_bounds__(256)
 
 // Query rows of a tile, by the rows of an average sequence (query tokens times
 // ratio): 8 for up to 8; else 32 where an even number of tiles of 16 holds them
-// and 16 where an odd one does; 16 for 256 elements, where the accumulators of
-// 32 rows do not fit in registers.  32 sequences of 4096 tokens, 8 heads, in us
-// as tiles of 32 / of 16 rows:
+// and 16 where an odd one does.  16 for 256 elements, where the accumulators of
+// 32 rows do not fit in registers, and for groups of 32 of 64 or 128 elements,
+// where they spill (up to 800 bytes a thread).  32 sequences of 4096 tokens, 8
+// heads, in us as tiles of 32 / of 16 rows:
 //   rows                  32          48          64          96
 //   128, one group      98 / 105   169 / 144   173 / 185   244 / 266
 //   128, groups of 64  112 / 124   199 / 176   201 / 226   289 / 335
 //   96, one group       83 / 90    141 / 122   145 / 157   205 / 225
 //   64, one group       74 / 73    131 / 98    133 / 126   180 / 180
+//   96, groups of 32   102 / 108   182 / 147   185 / 190   264 / 273
 //   128, groups of 32  196 / 153   362 / 223   369 / 288   538 / 426
 //   64, groups of 32   106 / 79    182 / 108   187 / 138   262 / 197
-// The last two, whose tiles of 32 rows spill registers (up to 800 bytes a
-// thread), would be better off with 16 throughout; the rule does not look at the
-// groups yet.
-inline int attention_row_tile(int head_dim, int64_t rows, int64_t batch, int ratio) {
+__host__ __device__ constexpr bool attention_has_tile_32(int head_dim, int group) {
+  return head_dim <= 128 && (group != 32 || head_dim == 96);
+}
+inline int attention_row_tile(int head_dim, int group, int64_t rows, int64_t batch, int ratio) {
   const int64_t r = (rows * ratio + batch - 1) / batch;
   if (r <= 8) return 8;
-  return head_dim > 128 || (r + 15) / 16 % 2 == 1 ? 16 : 32;
+  return !attention_has_tile_32(head_dim, group) || (r + 15) / 16 % 2 == 1 ? 16 : 32;
 }
 
 // Sets a kernel's dynamic shared memory once on each device.
@@ -1475,7 +1477,7 @@ bool with_attention_cfg(bool asym, int rt, F&& f) {
     if (asym) f(AttnCfg<D, GROUP, 2, true>{}); else f(AttnCfg<D, GROUP, 2, false>{});
     return true;
   }
-  if constexpr (D <= 128) {
+  if constexpr (attention_has_tile_32(D, GROUP)) {
     if (rt == 32) {
       if (asym) f(AttnCfg<D, GROUP, 4, true>{}); else f(AttnCfg<D, GROUP, 4, false>{});
       return true;

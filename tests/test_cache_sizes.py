@@ -35,3 +35,18 @@ def test_more_steps_than_32_bits_are_refused(L):
     for path in (q4.PATH_DECODE, q4.PATH_PREFILL):
         assert L.int4_cache_attention_workspace_size(c, 1, 1 << 24, 64, 1, 1 << 20, path,
                                                      ctypes.byref(size)) == q4.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("head_dim, group, tiles", [(128, 32, False), (64, 32, False), (256, 32, False), (256, 256, False),
+                                                    (128, 64, True), (128, 128, True), (64, 64, True), (96, 32, True)])
+def test_row_tiles_of_32_where_they_do_not_spill(L, head_dim, group, tiles):
+    """The workspace holds two pieces a block of the row tile's height: the same
+    for 16 and 32 rows a head where both take tiles of 16."""
+    sizes = []
+    for rows in (16, 32):
+        size = ctypes.c_size_t(0)
+        c = cache(pages=64, page_size=64, heads=8, head_dim=head_dim, group=group)
+        assert L.int4_cache_attention_workspace_size(c, 1, 32 * rows, 8, 32, 64, q4.PATH_DECODE,
+                                                     ctypes.byref(size)) == q4.OK
+        sizes.append(size.value)
+    assert (sizes[0] != sizes[1]) == tiles
