@@ -197,6 +197,32 @@ bool cache_prefill_supported(const CacheView& c, DType t, const void* out, int64
          mma_supported(c, t, out, rows, batch, ratio, max_pages, kPrefillRowTile);
 }
 
+// By head, groups and type, as the two kernels were measured: 32 sequences of
+// 4096 tokens, 8 heads, random codes, us with the kernels for few rows / with the
+// tcgen05 kernel:
+//   rows                         80          96         112         128         144
+//   128, one group          223 / 244   244 / 252   303 / 255   317 / 259   384 / 263
+//   128, groups of 64       274 / 342   287 / 345   373 / 348   374 / 349   471 / 352
+//   128, groups of 64, fp16 274 / 414   288 / 417   373 / 418   373 / 420   471 / 423
+//   128, groups of 32       344 / 343   425 / 344   466 / 347   557 / 348   596 / 350
+//   128, groups of 32, fp16 344 / 415   425 / 415   466 / 418   555 / 420   594 / 424
+//   96, one group           190 / 236   204 / 237   256 / 242   263 / 246   325 / 249
+//   96, groups of 32        230 / 257   264 / 260   313 / 263   343 / 269   398 / 268
+//   96, groups of 32, fp16  230 / 313   264 / 315   313 / 317   343 / 320   398 / 322
+//   64, one group           151 / 214   180 / 221   205 / 225   231 / 228   260 / 237
+//   64, groups of 32        166 / 235   196 / 238   225 / 243   254 / 244   284 / 250
+//   64, groups of 32, fp16  165 / 244   196 / 246   225 / 250   254 / 253   285 / 257
+// (types that are not named are alike).  One sequence alone, of 16384 tokens, would
+// be better off with the kernels for few rows up to 160 rows or so (heads of 128 in
+// one group: 128 rows 61 / 69, 160 69 / 74, 256 94 / 88).
+int cache_few_rows(const CacheView& c, DType t) {
+  const bool fp16 = t == DType::F16;
+  if (c.head_dim == 64) return 112;
+  if (c.head_dim == 128 && c.group == 64) return fp16 ? 128 : 96;
+  if (c.head_dim == 128 && c.group == 32) return fp16 ? 80 : 64;
+  return 96;
+}
+
 size_t cache_prefill_workspace(const CacheView& c, int64_t batch) {
   return attention_space_bytes(batch, num_sms(), kPrefillRowTile, c.head_dim);
 }

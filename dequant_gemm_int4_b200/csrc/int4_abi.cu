@@ -467,7 +467,7 @@ static int attention_plan(const char* name, const int4lib::CacheView& view, DTyp
   }
   if (asked == INT4_PATH_AUTO) {
     *path = !mma ? INT4_PATH_SIMT : INT4_PATH_DECODE;
-    if (prefill && batch > 0 && rows * ratio >= int4lib::kPrefillRows * static_cast<int64_t>(batch))
+    if (prefill && batch > 0 && rows * ratio > int4lib::cache_few_rows(view, t) * static_cast<int64_t>(batch))
       *path = INT4_PATH_PREFILL;
   }
   if (rows == 0 || batch == 0) return INT4_OK;

@@ -110,24 +110,9 @@ cudaError_t launch_cache_prefill(const AttentionArgs& a, DType t, void* workspac
 cudaError_t launch_cache_prefill_64(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
 cudaError_t launch_cache_prefill_96(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
 cudaError_t launch_cache_prefill_128(const AttentionArgs& a, DType t, void* workspace, cudaStream_t stream);
-// Query rows of one head (tokens times ratio) of an average sequence from which
-// it is taken.  32 sequences of 4096 tokens, 8 heads, random codes, us with the
-// kernels for few rows and with this one:
-//   rows                       64          96         128         256
-//   128, one group          173 / 239   244 / 250   316 / 259   598 / 298
-//   128, groups of 64       201 / 342   288 / 345   374 / 349   713 / 371
-//   128, groups of 64, fp16 201 / 412   288 / 415   375 / 419   714 / 441
-//   128, groups of 32       368 / 341   537 / 345   700 / 348  1353 / 367
-//   128, groups of 32, fp16 368 / 414   536 / 417   699 / 421  1357 / 440
-//   96, one group           145 / 225   204 / 234   263 / 246   495 / 282
-//   64, one group           132 / 213   180 / 221   232 / 225   432 / 258
-//   64, groups of 32        187 / 234   261 / 240   336 / 244   633 / 266
-// One sequence of 16384 tokens, 128 in one group: 128 rows 62 / 70, 256 94 / 88.
-// One value for all is right for heads of 128 in one group and in groups of 32 and
-// of 64 in groups of 32; the others meet between 96 and 150 rows, where a call
-// takes up to 23 % longer than it would with the kernel for few rows (44 % for
-// fp16 in groups of 64): the rule does not look at them yet.
-constexpr int kPrefillRows = 96;
+// Query rows of one head (tokens times ratio) of an average sequence up to which
+// the kernels for few rows are taken.
+int cache_few_rows(const CacheView& c, DType t);
 // cache_attention_<D>.cu: the kernels for heads of D elements; rt: query rows
 // of a tile.
 cudaError_t launch_cache_attention_64(const AttentionArgs& a, DType t, int rt, void* workspace, cudaStream_t stream);

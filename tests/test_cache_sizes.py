@@ -50,3 +50,20 @@ def test_row_tiles_of_32_where_they_do_not_spill(L, head_dim, group, tiles):
                                                      ctypes.byref(size)) == q4.OK
         sizes.append(size.value)
     assert (sizes[0] != sizes[1]) == tiles
+
+
+@pytest.mark.parametrize("head_dim, group, dtype, most", [
+    (128, 128, 1, 96), (128, 128, 2, 96), (128, 64, 1, 96), (128, 64, 2, 128), (128, 32, 1, 64), (128, 32, 2, 80),
+    (96, 96, 1, 96), (96, 32, 1, 96), (96, 32, 2, 96), (64, 64, 1, 112), (64, 32, 1, 112), (64, 32, 2, 112),
+    (256, 256, 1, 1 << 20)])
+def test_the_few_rows_kernel_is_taken_as_far_as_it_is_faster(L, head_dim, group, dtype, most):
+    def ask(rows, path):
+        size = ctypes.c_size_t(0)
+        c = cache(pages=64, page_size=64, heads=8, head_dim=head_dim, group=group)
+        rc = L.int4_cache_attention_workspace_size(c, dtype, 32 * rows, 8, 32, 64, path, ctypes.byref(size))
+        return size.value if rc == q4.OK else None
+
+    for rows in (1, 32, 64, 80, 96, 112, 128, 144, 256, 1000):
+        few, many = ask(rows, q4.PATH_DECODE), ask(rows, q4.PATH_PREFILL)
+        assert few != many
+        assert ask(rows, q4.PATH_AUTO) == (few if rows <= most else many), rows
