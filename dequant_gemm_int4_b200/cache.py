@@ -108,6 +108,9 @@ def int4_cache_attention(q: torch.Tensor, packed: torch.Tensor, scales: torch.Te
     ``sm_scale``: None is head_dim ** -0.5.  A query that sees nothing gets 0
     and -inf; rows of no sequence are left as they were.
 
+    ``path``: PATH_AUTO takes a tensor-core kernel where one can run (16-bit q;
+    weights rounded to fp16); PATH_SIMT the general kernel, in fp32 throughout;
+    PATH_DECODE and PATH_PREFILL a given tensor-core kernel.
     ``workspace``: None takes one from torch's allocator for this call; a uint8
     CUDA tensor of cache_attention_workspace_size bytes is used as given."""
     r = (_binding or _native()).attention(q, packed, scales, page_table, kv_lens, group, zeros, q_starts,

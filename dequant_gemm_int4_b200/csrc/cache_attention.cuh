@@ -1210,9 +1210,9 @@ __global__ void __launch_bounds__(256)
 }
 
 // The join by items, where a sequence has several row tiles (and for the large
-// ones of the tcgen05 kernel): block (c, i) joins rows [8 i, 8 i + 8) of the item that begins in share
-// c and goes on in the next ones, if there is one; blocks (ws.blocks + b, i)
-// write the rows of sequence b's tiles that see nothing.
+// ones of the tcgen05 kernel): block (c, i) joins rows [8 i, 8 i + 8) of the item
+// that begins in share c and goes on in the next ones, if there is one; blocks
+// (ws.blocks + b, i) write the rows of sequence b's tiles that see nothing.
 template <typename T>
 __global__ void __launch_bounds__(256)
     attention_join_items_kernel(const __grid_constant__ AttentionArgs a, const AttentionSpace ws, const int RT) {

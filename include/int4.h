@@ -429,13 +429,13 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * sm_scale   finite.
  *
  * Accuracy: S (of any size that fp32 holds), the softmax's maximum and sum, and
- * out's sums are fp32.  For
- * fp32 q so are the products.  For bf16 and fp16 q the products run on tensor
- * cores: q and the codes exactly (elements of q below 2^-24 of the row's
- * largest to 2^-38 of it), the weights exp(S_j - max) s_j, s_j the value
- * scales, in fp16 after two roundings, each off by at most 2^-11 of the value,
- * or, below 2^-20 s, by 2^-31 s, where s is the largest value scale and lies
- * between 2^-8 and 2^8 (2^-24 s for larger, 2^-40 for smaller ones).
+ * out's sums are fp32.  For fp32 q so are the products.  For bf16 and fp16 q the
+ * products run on tensor cores: q and the codes exactly (elements of q below
+ * 2^-24 of the row's largest to 2^-38 of it), the weights exp(S_j - max) s_j, s_j
+ * the value scales, in fp16 after two roundings, each off by at most 2^-11 of the
+ * value, or, below 2^-20 s, by 2^-31 s, where s is the largest value scale of the
+ * tokens taken together and lies between 2^-8 and 2^8 (2^-24 s for larger, 2^-40
+ * for smaller ones).
  * INT4_PATH_DECODE sums the codes and the zero points z (8 in the symmetric
  * scheme) apart, and its outputs are off by up to 2^-13 of sum_j p_j s_j z_j too,
  * p_j = exp(S_j - lse).  INT4_PATH_PREFILL rounds the weight once; with several
@@ -449,12 +449,13 @@ int int4_cache_read(const int4_cache* cache, const int64_t* slots, int64_t token
  * infinity, minus infinity or NaN.
  *
  * `path`: INT4_PATH_AUTO takes a tensor-core kernel where one can run, else the
- * general kernel (INT4_PATH_SIMT).  INT4_PATH_DECODE, for few query rows: bf16 or
- * fp16 q, head_dim 64, 96, 128 or 256 in groups of 32, 64, 128 or head_dim (96:
- * 32 or 96), page_size a power of two from 16 on, max_pages * page_size <= 2^30
- * (and the table's steps of 128 tokens, for each tile of 8, 16 or 32 rows of
- * every head, below 2^31), packed, scales and zeros 16-byte and out 8-byte
- * aligned.  INT4_PATH_PREFILL, for many: of those, with tiles of 256 rows,
+ * general kernel (INT4_PATH_SIMT, which takes every call, with fp32 products and
+ * weights for all types, and is many times slower).  INT4_PATH_DECODE, for few
+ * query rows: bf16 or fp16 q, head_dim 64, 96, 128 or 256 in groups of 32, 64, 128
+ * or head_dim (96: 32 or 96), page_size a power of two from 16 on, max_pages *
+ * page_size <= 2^30 (and the table's steps of 128 tokens, for each tile of 8, 16
+ * or 32 rows of every head, below 2^31), packed, scales and zeros 16-byte and out
+ * 8-byte aligned.  INT4_PATH_PREFILL, for many: of those, with tiles of 256 rows,
  * head_dim 64, 96 or 128, out 16-byte aligned.  A forced path that cannot run
  * the call returns INT4_ERR_UNSUPPORTED.
  *
